@@ -326,7 +326,8 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
       *reinterpret_cast<hE *>(dst) = y;
       if constexpr (NP == 2) *reinterpret_cast<hE *>(dst + PART) = z;
       if ((tid & 15) == 0) {
-        (which == 0 ? sk : su)[i] = rest;
+        // (past the end rows of zeros stand in, whose norm without eps is 1 / 0: they weigh nothing)
+        (which == 0 ? sk : su)[i] = i < n ? rest : 0.f;
         // (the state's pass reads a row in the place of those past the end)
         if (which == 0) reinterpret_cast<float *>(rec + Rec::kf)[i] = i < n ? f : 0.f;
       }

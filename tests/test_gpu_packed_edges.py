@@ -1,0 +1,55 @@
+"""The packed calls away from their defaults: other eps, values of very different sizes along the
+tokens, values that are not finite, and what a call may be given."""
+import pytest
+
+import _packed_ref as R
+
+pytestmark = pytest.mark.gpu
+
+ENTRIES = ["step", "generic", "mfma"]
+
+
+def run(x, entry, **kw):
+    """An entry point on the case (``kw``: further arguments); returns (out, pool)."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    d = {n: t.cuda() if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+    out = torch.full(x["v"].shape, 7.0, dtype=x["v"].dtype, device="cuda")
+    kw = dict(dict(beta=d["beta"], log_alpha=d["log_alpha"], state_index=d["index"], has_state=d["has"], qk_norm=x["qk_norm"],
+                   norm_weight=d["norm_weight"], norm_gate=d["norm_gate"], out=out, scale=x["scale"]), **kw)
+    print(f"[case] {entry} lens {x['lens'][:8]} q {tuple(x['q'].shape)} v {tuple(x['v'].shape)} {x['q'].dtype}", flush=True)
+    if entry == "step":
+        G.gdr_packed_step(d["q"], d["k"], d["v"], d["pool"], cu_seqlens=d["cu"], **kw)
+    else:
+        G.gdr_packed_fwd(d["q"], d["k"], d["v"], d["cu"], state=d["pool"], impl=entry, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), d["pool"].cpu()
+
+
+def io_tol(x, entry):
+    """One rounding to the type; bf16 outputs of the chunked kernel take one fp16 part each of P, E and S."""
+    import torch
+    io = x["v"].dtype
+    return R.half_step(io) + (2.0 ** -11 if entry == "mfma" and io == torch.bfloat16 else 0.0)
+
+
+def normalised(x, eps):
+    """The case with q and k over their L2 norms in 64 bits."""
+    q, k = x["q"].double(), x["k"].double()
+    return dict(x, q=q / (q.square().sum(-1, keepdim=True) + eps).sqrt(), k=k / (k.square().sum(-1, keepdim=True) + eps).sqrt(),
+                qk_norm=False)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("eps", [0.0, 1e-3, 2.0])
+@pytest.mark.parametrize("lens", [[1], [63], [64], [65], [130, 5, 0, 64]], ids=str)
+def test_key_norm_eps(entry, io, eps, lens):
+    """eps = 0 too: rows past a sequence's end are no keys of size 0."""
+    import torch
+    x = R.make(lens, Hk=2, Hv=4, Dk=64, Dv=32, io=io, qk_norm=True, seed=81 + len(lens))
+    out, pool = run(x, entry, qk_eps=eps)
+    ref_o, ref_p = R.delta(normalised(x, eps), torch.zeros(x["v"].shape))
+    tol = R.state_tol(max(lens))
+    assert R.rel(pool, ref_p) <= tol
+    assert R.rel(out, ref_o) <= io_tol(x, entry) + tol
