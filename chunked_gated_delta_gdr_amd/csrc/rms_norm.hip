@@ -271,7 +271,8 @@ __global__ __launch_bounds__(threads_of(LANES), bwd_waves(LANES, IT, kVec<IO>)) 
       }
     }
     row_sum2<LANES>(ss, uh, red + turn);
-    const float r = rsqrt_f(ss * a.inv_d + a.eps);
+    // (lanes without a row hold zeros, whose 1 / sqrt(0) without eps must not reach dw)
+    const float r = live ? rsqrt_f(ss * a.inv_d + a.eps) : 0.f;
     const float mean = uh * r * a.inv_d;   // mean(u (.) n)
     if (kTwice) asm volatile("" ::: "memory");   // the second loads stay loads
 #pragma unroll

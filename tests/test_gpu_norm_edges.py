@@ -1,0 +1,40 @@
+"""The norms away from their defaults: eps = 0, infinite values under 8-bit outputs, far gates."""
+import pytest
+
+import _packed_ref as R
+from test_gpu_norm import GATE, STAT, dev, make
+
+pytestmark = pytest.mark.gpu
+
+
+# widths of every number of lanes a row up to 64, which share a workgroup with other rows, and one wider
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("loads", [1, 8, 16, 31, 33, 48, 64, 65, 96, 128, 129, 192, 193, 256])
+@pytest.mark.parametrize("rows", [1, 5, 33])
+@pytest.mark.parametrize("gate", [False, True])
+def test_gradient_without_eps(io, loads, rows, gate):
+    """Lanes without a row add nothing to the weight's gradient, whatever 1 / sqrt(0) is."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    D = loads * (4 if io == "f32" else 8) - loads % 2
+    x = make(rows, D, io, gate=gate, seed=rows + D)
+    dy = torch.randn(rows, D, generator=torch.Generator().manual_seed(3), dtype=torch.float64).to(R.IO[io])
+    leaves = [x[n].double().requires_grad_() for n in ("x", "weight", "gate") if x[n] is not None]
+    y, _ = R.norm(leaves[0], weight=leaves[1], gate=leaves[2] if gate else None, eps=0.0)
+    grads = torch.autograd.grad((y * dy.double()).sum(), leaves)
+    d = dev(x)
+    got = G.gdr_rms_norm_bwd(d["x"], dy.cuda(), weight=d["weight"], gate=d["gate"], eps=0.0)
+    out = G.gdr_rms_norm(d["x"], weight=d["weight"], gate=d["gate"], eps=0.0)[0]
+    half = R.half_step(R.IO[io])
+    assert R.rel(out.cpu(), y.detach()) <= half + STAT + GATE
+    n = leaves[0].detach() / leaves[0].detach().square().mean(-1, keepdim=True).sqrt()
+    act = 1.0 if not gate else (x["gate"].double() * torch.sigmoid(x["gate"].double())).abs()
+    size = (dy.double().abs() * act * n.abs()).sum(0)
+    assert ((got["dweight"].cpu().double() - grads[1]).abs() <= 2 * (STAT + GATE) * size + 1e-30).all()
+    u = dy.double().abs() * x["weight"].double().abs() * act
+    r = 1 / leaves[0].detach().square().mean(-1, keepdim=True).sqrt()
+    terms = r * (u + n.abs() * (u * n.abs()).mean(-1, keepdim=True))
+    err = (got["dx"].cpu().double() - grads[0]).abs()
+    assert (err <= half * grads[0].abs() + 2 * (STAT + GATE) * terms + 2.0 ** -24).all()
+    if gate:
+        assert torch.isfinite(got["dgate"].float()).all()
