@@ -15,7 +15,7 @@ using gdr::host::rng;
 namespace {
 
 constexpr long long kMaxStreams = 1LL << 18;   // (sequence, value head) pairs: 2^31 work-items at Dv = 512
-constexpr long long kMaxRows = 1LL << 26;      // (token, value head) pairs: grids of 2^32 work-items
+constexpr long long kMaxRows = 1LL << 26;      // (token, value head) pairs
 constexpr long long kMaxStride = 1LL << 23;    // elements between the tokens of a packed tensor
 constexpr int kMaxD = 16384;                   // channels of a norm's row
 

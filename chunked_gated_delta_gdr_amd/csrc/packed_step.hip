@@ -238,11 +238,7 @@ hipError_t launch_io(const PackedArgs &a, hipStream_t s) {
 // row's columns, and for Dv > 256.  A row is (token, head), 64 lanes a row, Dv <= 512; it reads and
 // writes what the kernel before left in the caches.
 template <typename IO>
-__global__ __launch_bounds__(256) void packed_norm_kernel(PackedArgs a) {
-  const int lane = threadIdx.x & 63;
-  const long long row = blockIdx.x * 4ll + (threadIdx.x >> 6);
-  const int t = static_cast<int>(row / a.Hv), h = static_cast<int>(row % a.Hv);
-  if (t >= a.N) return;
+__device__ __forceinline__ void norm_row(const PackedArgs &a, int t, int h, int lane) {
   int s = t;
   if (a.cu != nullptr) {   // the last sequence that begins at or before t
     int lo = 0, hi = a.n_seqs;
@@ -278,6 +274,15 @@ __global__ __launch_bounds__(256) void packed_norm_kernel(PackedArgs a) {
   }
 }
 
+// Workgroups of a launch, at most: its work-items have to stay below 2^32
+constexpr long long kNormGroups = 1ll << 23;
+template <typename IO>
+__global__ __launch_bounds__(256) void packed_norm_kernel(PackedArgs a) {
+  const long long rows = static_cast<long long>(a.N) * a.Hv;
+  for (long long row = blockIdx.x * 4ll + (threadIdx.x >> 6); row < rows; row += gridDim.x * 4ll)
+    norm_row<IO>(a, static_cast<int>(row / a.Hv), static_cast<int>(row % a.Hv), threadIdx.x & 63);
+}
+
 }  // namespace
 
 hipError_t launch_packed_recur(const PackedArgs &a, int io_dtype, hipStream_t s) {
@@ -290,7 +295,7 @@ hipError_t launch_packed_recur(const PackedArgs &a, int io_dtype, hipStream_t s)
 hipError_t launch_packed_norm(const PackedArgs &a, int io_dtype, hipStream_t s) {
   const long long rows = static_cast<long long>(a.N) * a.Hv;
   if (rows == 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), block(256);
+  const dim3 grid(static_cast<unsigned>(rows < 4 * kNormGroups ? (rows + 3) / 4 : kNormGroups)), block(256);
   if (io_dtype == GDR_BF16)
     hipLaunchKernelGGL((packed_norm_kernel<uint16_t>), grid, block, 0, s, a);
   else if (io_dtype == GDR_F16)

@@ -53,3 +53,23 @@ def test_key_norm_eps(entry, io, eps, lens):
     tol = R.state_tol(max(lens))
     assert R.rel(pool, ref_p) <= tol
     assert R.rel(out, ref_o) <= io_tol(x, entry) + tol
+
+
+def test_output_norm_of_the_most_rows():
+    """n_tokens * Hv at its limit, 2^26: the norm's launch has its rows too."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    x = R.make([70], Hk=1, Hv=32, Dk=8, Dv=8, norm=True, seed=85)
+    want_o, want_p = run(x, "mfma")
+    N = 2 ** 26 // 32
+    at = {n: torch.zeros((N,) + x[n].shape[1:], dtype=x[n].dtype, device="cuda") for n in ("q", "k", "v", "beta", "log_alpha")}
+    for n, t in at.items():
+        t[N - 70:] = x[n].cuda()
+    out = torch.full((N, 32, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    pool = x["pool"].cuda()
+    cu = torch.tensor([N - 70, N], dtype=torch.int32, device="cuda")
+    G.gdr_packed_fwd(at["q"], at["k"], at["v"], cu, beta=at["beta"], log_alpha=at["log_alpha"], state=pool, scale=x["scale"],
+                     norm_weight=x["norm_weight"].cuda(), out=out, impl="mfma")
+    torch.cuda.synchronize()
+    assert torch.equal(out[N - 70:].cpu(), want_o) and torch.equal(pool.cpu(), want_p)
+    assert bool((out[:N - 70] == 7.0).all())

@@ -206,3 +206,13 @@ def test_cpu_tensors_are_refused():
         G.gdr_packed_step(q, q, q, torch.zeros(4, 2, 8, 8), beta=torch.zeros(4, 2))
     with pytest.raises(ValueError):
         G.gdr_packed_fwd(q, q, q, torch.zeros(2, dtype=torch.int32), beta=torch.zeros(4, 2))
+
+
+def test_most_rows_of_a_packed_call():
+    """n_tokens * Hv: 2^26 is the last that both take, with the output norm's launch too."""
+    ins = pins(norm_weight=at(8), q=1 << 40, k=1 << 41, v=1 << 42, beta=1 << 43, log_alpha=1 << 44)
+    for step in (False, True):
+        d = pdesc(n_tokens=1 << 21, Hk=1, Hv=32, Dk=8, Dv=8)
+        pcheck(G.GDR_OK, d=d, ins=ins, out=1 << 45, ws=1 << 46, ws_bytes=1 << 40, for_step=step)
+        d.n_tokens += 1
+        pcheck(G.GDR_ENOTSUP, d=d, ins=ins, out=1 << 45, ws=1 << 46, ws_bytes=1 << 40, for_step=step)
