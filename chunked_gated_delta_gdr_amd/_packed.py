@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from typing import Optional, Tuple
 
 import torch
@@ -156,16 +157,25 @@ class _On:
 
 
 def _placed(call):
-    """Runs ``call(x, ..)`` with x's device current, on ``stream`` where one is given."""
+    """Adds ``stream`` to ``call``'s keyword arguments: it runs with its first argument's device
+    current, on ``stream`` where one is given."""
+    sig = inspect.signature(call)
+    first = next(iter(sig.parameters))
+
     @functools.wraps(call)
-    def placed(x, *args, stream=None, **kw):
+    def placed(*args, stream=None, **kw):
+        x = args[0] if args else kw.get(first)
+        if x is None:
+            return call(*args, **kw)   # (names what is missing)
         index = x.get_device()
         if index < 0:
             raise ValueError(f"tensors must be on a GPU, not on {x.device}")
         if stream is None and torch.cuda.current_device() == index:
-            return call(x, *args, **kw)
+            return call(*args, **kw)
         with _On(x.device, stream):
-            return call(x, *args, **kw)
+            return call(*args, **kw)
+    placed.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(), inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return placed
 
 

@@ -73,3 +73,21 @@ def test_output_norm_of_the_most_rows():
     torch.cuda.synchronize()
     assert torch.equal(out[N - 70:].cpu(), want_o) and torch.equal(pool.cpu(), want_p)
     assert bool((out[:N - 70] == 7.0).all())
+
+
+@pytest.mark.parametrize("entry", ["fwd", "step"])
+def test_every_tensor_by_name(entry):
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    x = R.make([3, 2], seed=86)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "beta", "log_alpha")}
+    d.update(cu_seqlens=x["cu"].cuda(), scale=x["scale"])
+    want = run(x, "step" if entry == "step" else "mfma")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        pool = x["pool"].cuda()
+        torch.cuda.synchronize()
+        got = getattr(G, f"gdr_packed_{entry}")(state=pool, stream=stream, **d)
+        torch.cuda.synchronize()
+        assert torch.equal(got.cpu(), want[0]) and torch.equal(pool.cpu(), want[1])

@@ -216,3 +216,23 @@ def test_most_rows_of_a_packed_call():
         pcheck(G.GDR_OK, d=d, ins=ins, out=1 << 45, ws=1 << 46, ws_bytes=1 << 40, for_step=step)
         d.n_tokens += 1
         pcheck(G.GDR_ENOTSUP, d=d, ins=ins, out=1 << 45, ws=1 << 46, ws_bytes=1 << 40, for_step=step)
+
+
+def test_arguments_by_name():
+    """Every tensor may be named, the first too, and the signatures say that a stream may be given."""
+    import inspect
+    import torch
+    q = torch.zeros(4, 2, 8)
+    cu = torch.zeros(2, dtype=torch.int32)
+    calls = [(G.gdr_packed_fwd, dict(q=q, k=q, v=q, cu_seqlens=cu, beta=q[..., 0])),
+             (G.gdr_packed_step, dict(q=q, k=q, v=q, state=torch.zeros(4, 2, 8, 8), beta=q[..., 0])),
+             (G.gdr_rms_norm, dict(x=q[0])), (G.gdr_rms_norm_bwd, dict(x=q[0], dy=q[0]))]
+    for call, kw in calls:
+        with pytest.raises(ValueError, match="must be on a GPU"):
+            call(**kw)
+        first = next(iter(kw))
+        with pytest.raises(TypeError, match=f"'{first}'"):
+            call(**{n: t for n, t in kw.items() if n != first})
+        stream = inspect.signature(call).parameters["stream"]
+        assert stream.kind is inspect.Parameter.KEYWORD_ONLY and stream.default is None
+        assert list(inspect.signature(call).parameters)[0] == first
