@@ -63,7 +63,8 @@ def _lib() -> ctypes.CDLL:
 
 
 # ------------------------------------------------------------------------------------
-# descriptors: by value, so that calls of one shape share them
+# descriptors: by value, so that calls of one shape share them (fields are plain numbers: a tensor
+# would be found again by its identity, whatever it holds by then)
 # ------------------------------------------------------------------------------------
 
 @functools.lru_cache(maxsize=1024)
@@ -265,7 +266,7 @@ def _packed(q, k, v, n_seqs, cu_seqlens, beta, log_alpha, state, state_index, ha
         _flat("norm_weight", norm_weight, (Dv,), (io,), index),
         None if norm_gate is None else norm_gate.data_ptr())
     fields = (N, n_seqs, Hk, Hv, Dk, Dv, slots, code, B.GDR_DECAY_NONE if log_alpha is None else B.GDR_DECAY_SCALAR,
-              int(qk_norm), impl, scale, qk_eps, norm_eps, qs, ks, vs, os_, zs)
+              int(qk_norm), impl, float(scale), float(qk_eps), float(norm_eps), qs, ks, vs, os_, zs)
     return fields, ins, pool
 
 
@@ -348,7 +349,7 @@ def gdr_rms_norm(x, *, weight=None, residual=None, gate=None, out_dtype=None, ou
     else:
         total = _flat("residual_out", residual_out, shape, (io,), index)
     st = _lib().gdr_rms_norm(
-        _norm_desc(rows, D, code, kind, eps, xs, rs, zs, 0), x.data_ptr(),
+        _norm_desc(rows, D, code, kind, float(eps), xs, rs, zs, 0), x.data_ptr(),
         None if residual is None else residual.data_ptr(), _flat("weight", weight, (D,), (io,), index),
         None if gate is None else gate.data_ptr(), y, sc, total, _raw_stream(index))
     if st:
@@ -371,7 +372,7 @@ def gdr_rms_norm_bwd(x, dy, *, weight=None, gate=None, d_residual=None, want_dwe
     xs, ds = _rows("x", x, shape, D, io, index), _rows("dy", dy, shape, D, io, index)
     rs = 0 if d_residual is None else _rows("d_residual", d_residual, shape, D, io, index)
     zs = 0 if gate is None else _rows("gate", gate, shape, D, io, index)
-    desc = _norm_desc(rows, D, code, GDR_OUT_IO, eps, xs, rs, zs, ds)
+    desc = _norm_desc(rows, D, code, GDR_OUT_IO, float(eps), xs, rs, zs, ds)
     g = {"dx": _new_rows(x, io)}
     ws, nbytes = None, 0
     if weight is not None and want_dweight:

@@ -38,3 +38,15 @@ def test_gradient_without_eps(io, loads, rows, gate):
     assert (err <= half * grads[0].abs() + 2 * (STAT + GATE) * terms + 2.0 ** -24).all()
     if gate:
         assert torch.isfinite(got["dgate"].float()).all()
+
+
+def test_eps_may_be_a_tensor_that_changes():
+    """Its value at the call counts, not the one that an earlier call met."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    d = dev(make(3, 40, "f32", seed=2))
+    eps = torch.tensor(0.0)
+    for value in (1e-6, 3.0, 100.0):
+        eps.fill_(value)
+        assert torch.equal(G.gdr_rms_norm(d["x"], eps=eps)[0], G.gdr_rms_norm(d["x"], eps=value)[0])
+        assert torch.equal(G.gdr_rms_norm_bwd(d["x"], d["x"], eps=eps)["dx"], G.gdr_rms_norm_bwd(d["x"], d["x"], eps=value)["dx"])

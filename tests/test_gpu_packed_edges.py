@@ -91,3 +91,16 @@ def test_every_tensor_by_name(entry):
         got = getattr(G, f"gdr_packed_{entry}")(state=pool, stream=stream, **d)
         torch.cuda.synchronize()
         assert torch.equal(got.cpu(), want[0]) and torch.equal(pool.cpu(), want[1])
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_scale_and_eps_may_be_tensors_that_change(entry):
+    """Their values at the call count, not those that an earlier call met."""
+    import torch
+    x = R.make([3, 2], qk_norm=True, norm=True, seed=84)
+    t = {n: torch.tensor(0.0) for n in ("scale", "qk_eps", "norm_eps")}
+    for values in (dict(scale=0.5, qk_eps=1e-6, norm_eps=1e-2), dict(scale=3.0, qk_eps=2.0, norm_eps=5.0)):
+        for n, v in values.items():
+            t[n].fill_(v)
+        got, want = run(x, entry, **t), run(x, entry, **values)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
