@@ -254,6 +254,8 @@ def _packed(q, k, v, n_seqs, cu_seqlens, beta, log_alpha, state, state_index, ha
     slots, pool = 0, None
     if state is not None:
         slots = state.shape[0]
+        if slots == 0 and n_seqs > 0:   # (its pointer is null, which means no pool at all)
+            raise ValueError("state has no slots")
         pool = _flat("state", state, (slots, Hv, Dv, Dk), _F32, index)
     if beta is None:
         raise ValueError("beta is required")

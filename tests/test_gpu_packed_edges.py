@@ -104,3 +104,13 @@ def test_scale_and_eps_may_be_tensors_that_change(entry):
             t[n].fill_(v)
         got, want = run(x, entry, **t), run(x, entry, **values)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_a_pool_without_slots_is_refused(entry):
+    """It is no missing pool, with which sequences start from zeros."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    x = R.make([3, 2], slots=2, index=[0, 1], seed=83)
+    with pytest.raises((ValueError, G.GdrError)):
+        run(dict(x, pool=x["pool"][:0]), entry)
