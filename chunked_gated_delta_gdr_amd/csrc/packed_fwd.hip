@@ -310,7 +310,9 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
         ss = sum16(ss);
-        rest = rsqrt_f(ss + a.qk_eps * f * f);
+        const float eps = a.qk_eps * f * f;
+        // (a row so far below eps that eps leaves the type on the row's scale: 2^-ex / sqrt(2^(-2 ex) eps) = 1 / sqrt(eps))
+        rest = eps < __int_as_float(0x7f800000) ? rsqrt_f(ss + eps) : rsqrt_f(a.qk_eps) * rest;
         if (ss == 0.f && a.qk_eps == 0.f) rest = __int_as_float(0x7fc00000);   // 0 / 0
       }
       typedef _Float16 hE __attribute__((ext_vector_type(E)));

@@ -114,3 +114,20 @@ def test_a_pool_without_slots_is_refused(entry):
     x = R.make([3, 2], slots=2, index=[0, 1], seed=83)
     with pytest.raises((ValueError, G.GdrError)):
         run(dict(x, pool=x["pool"][:0]), entry)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-12, 1e-20, 1e-24, 1e-30])
+def test_tiny_keys_under_the_norm(entry, io, size):
+    """Keys and queries far below eps's root: k / sqrt(eps), as small as it is."""
+    import torch
+    x = R.make([70, 2], Dk=64, Dv=32, io=io, qk_norm=True, has=[False, False], seed=82)
+    for n in "qk":
+        x[n] = (x[n].double() * size).to(x[n].dtype)
+    x["scale"] = 1.0 / (1e3 * size)   # (outputs of v's size times k's)
+    out, pool = run(x, entry)
+    ref_o, ref_p = R.delta(normalised(x, 1e-6), torch.zeros(x["v"].shape))
+    assert R.rel(pool, ref_p) <= R.state_tol(70)
+    if size >= 1e-12:   # (beyond, the output's own products leave fp32's range or io's)
+        assert R.rel(out, ref_o) <= io_tol(x, entry) + R.state_tol(70)
