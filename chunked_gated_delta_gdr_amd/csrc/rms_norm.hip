@@ -176,6 +176,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void norm_kernel(NormArgs a) {
   float scale = row_max<LANES>(m, red[1]) / (fp8 ? 448.f : 127.f);
   if (scale < 1.17549435e-38f) scale = 0.f;   // a row of zeros (or one whose reciprocal scale would overflow)
   const float inv = scale == 0.f ? 0.f : 1.f / scale;
+  const float step = scale < __int_as_float(0x7f800000) ? scale : 0.f;   // (an infinite one: finite y / s are 0, not 0 * inf)
   if (live && l == 0) a.scales[row] = scale;
   uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.D;
 #pragma unroll
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {   // y / s to the last bit or so: a product, and its rest
       const float c0 = h[i][e] * inv;
-      h[i][e] = fmaf(fmaf(-c0, scale, h[i][e]), inv, c0);
+      h[i][e] = fmaf(fmaf(-c0, step, h[i][e]), inv, c0);
     }
 #pragma unroll
     for (int e = 0; e < V; e += 4) w[e / 4] = fp8 ? pack_fp8(h[i] + e) : pack_int8(h[i] + e);

@@ -456,7 +456,8 @@ typedef struct gdr_norm_desc {
  *   weight             [D] io_dtype, or NULL (ones)
  *   y                  [rows, D] io_dtype; or, in 8 bits, codes whose value is code * scales[row]
  *   scales             [rows] fp32, iff out_kind is 8 bits: max |y| / 127 (int8) or / 448 (e4m3);
- *                      0 for a row of zeros (its codes are 0), NaN for one that holds a NaN
+ *                      0 for a row of zeros (its codes are 0), NaN where a y is NaN, else infinite where
+ *                      one is infinite (the finite ones' codes are 0)
  *   residual_out       [rows, D] io_dtype, x + residual rounded; required iff residual is given.
  *                      May be the same pointer as x or residual, with the same row stride.
  * The norm is taken of the fp32 sum.  y may be x where the types and strides agree and there is

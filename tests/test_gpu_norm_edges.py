@@ -50,3 +50,24 @@ def test_eps_may_be_a_tensor_that_changes():
         eps.fill_(value)
         assert torch.equal(G.gdr_rms_norm(d["x"], eps=eps)[0], G.gdr_rms_norm(d["x"], eps=value)[0])
         assert torch.equal(G.gdr_rms_norm_bwd(d["x"], d["x"], eps=eps)["dx"], G.gdr_rms_norm_bwd(d["x"], d["x"], eps=value)["dx"])
+
+
+@pytest.mark.parametrize("codes", ["int8", "float8_e4m3fn"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+def test_eight_bit_codes_beside_an_infinity(codes, bad):
+    """An infinite value makes its row's scale infinite and the finite ones' codes 0, and nothing else of it."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    for D in (7, 300, 2048):
+        x = make(4, D, "f32", gate=True, weight=False, seed=D)
+        x["gate"] = x["gate"].abs() + 0.1
+        want = [t.cpu() for t in G.gdr_rms_norm(out_dtype=getattr(torch, codes), **dev(x))[:2]]
+        x["x"][2, 5] = x["x"][2, 5].abs() + 0.1
+        x["gate"][2, 5] = abs(bad)   # silu(inf) = inf
+        x["x"][2, 5] *= 1.0 if bad > 0 else -1.0
+        out, scales = (t.cpu() for t in G.gdr_rms_norm(out_dtype=getattr(torch, codes), **dev(x))[:2])
+        assert scales[2] == float("inf")
+        rest = [i for i in range(D) if i != 5]
+        assert (out[2, rest].float() == 0).all()
+        keep = [0, 1, 3]
+        assert torch.equal(out[keep].view(torch.uint8), want[0][keep].view(torch.uint8)) and torch.equal(scales[keep], want[1][keep])
