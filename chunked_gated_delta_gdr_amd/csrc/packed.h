@@ -127,9 +127,12 @@ __device__ __forceinline__ float rsqrt_f(float x) {
   return tiny ? r * 0x1p32f : r;
 }
 
-// (within 2^-22 of themselves for |z| of a few; 0 and 1 far out)
-__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
-__device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f(z); }
+// Of a gate held in IO.  The fast exponential is off by 2^-24 |z| of itself: nothing next to a 16-bit
+// gate's own rounding, up to 44 roundings of an fp32 one, which takes the exact one.  0 and 1 far out.
+template <typename IO> __device__ __forceinline__ float sigmoid_f(float z) {
+  return __builtin_amdgcn_rcpf(1.f + (sizeof(IO) == 4 ? expf(-z) : __expf(-z)));
+}
+template <typename IO> __device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f<IO>(z); }
 
 // ---------------------------------------------------------------------------------
 // A sequence's tokens and slot.  Device values are clamped into range, so that a bad one

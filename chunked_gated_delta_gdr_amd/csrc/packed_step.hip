@@ -185,7 +185,7 @@ __global__ __launch_bounds__(THREADS, THREADS == kWide ? 2 : DK == 64 ? 5 : 3) v
       const float r = rsqrt_f(all / a.Dv + a.norm_eps);
       if (lane < mine) {
         ov *= r * to_f(static_cast<const IO *>(a.norm_w)[row0 + lane]);
-        if (a.norm_z != nullptr) ov *= silu_f(to_f(static_cast<const IO *>(a.norm_z)[t * a.zs + h * a.Dv + row0 + lane]));
+        if (a.norm_z != nullptr) ov *= silu_f<IO>(to_f(static_cast<const IO *>(a.norm_z)[t * a.zs + h * a.Dv + row0 + lane]));
       }
     }
     if (lane < mine) out[t * a.os] = from_f<IO>(ov);
@@ -269,7 +269,7 @@ __device__ __forceinline__ void norm_row(const PackedArgs &a, int t, int h, int 
     const int c = lane + 64 * j;
     if (c >= a.Dv) continue;
     float y = x[j] * r * to_f(static_cast<const IO *>(a.norm_w)[c]);
-    if (a.norm_z != nullptr) y *= silu_f(to_f(static_cast<const IO *>(a.norm_z)[t * a.zs + static_cast<long long>(h) * a.Dv + c]));
+    if (a.norm_z != nullptr) y *= silu_f<IO>(to_f(static_cast<const IO *>(a.norm_z)[t * a.zs + static_cast<long long>(h) * a.Dv + c]));
     o[c] = from_f<IO>(y);
   }
 }

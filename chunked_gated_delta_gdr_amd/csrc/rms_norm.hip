@@ -162,7 +162,7 @@ __global__ __launch_bounds__(threads_of(LANES)) void norm_kernel(NormArgs a) {
     if (z != nullptr) {
       load_row<V>(z, c, D, g);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[i][e] *= silu_f(g[e]);
+      for (int e = 0; e < V; ++e) h[i][e] *= silu_f<IO>(g[e]);
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) m = c + e < D ? max_nan(m, fabsf(h[i][e])) : m;
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(threads_of(LANES), bwd_waves(LANES, IT, kVec<IO>)) 
         if (a.w == nullptr) w[j][e] = 1.f;
         u[j][e] = to_f(static_cast<IO>(ur[i][e]));
         if (kGate) {
-          const float g = dz[j][e], sg = sigmoid_f(g);
+          const float g = dz[j][e], sg = sigmoid_f<IO>(g);
           dz[j][e] = u[j][e] * w[j][e] * sg * (1.f + g * (1.f - sg));
           u[j][e] *= g * sg;
         }

@@ -71,3 +71,27 @@ def test_eight_bit_codes_beside_an_infinity(codes, bad):
         assert (out[2, rest].float() == 0).all()
         keep = [0, 1, 3]
         assert torch.equal(out[keep].view(torch.uint8), want[0][keep].view(torch.uint8)) and torch.equal(scales[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("D", [64, 1000, 4096])
+def test_far_gates_in_fp32(D):
+    """silu and its slope keep fp32's relative precision out to where the exponential leaves the type."""
+    import torch
+    import chunked_gated_delta_gdr_amd as G
+    x = make(9, D, "f32", gate=True, seed=D)
+    x["gate"] = (torch.arange(9 * D, dtype=torch.float64).reshape(9, D) / (9 * D) * 160 - 80).float()
+    d = dev(x)
+    y, _ = R.norm(**x)
+    # one rounding, the row's statistic, and 8 roundings of exp, the sum, the reciprocal and the products
+    tol = R.half_step(torch.float32) * (1 + 8) + STAT
+    err = (G.gdr_rms_norm(**d)[0].cpu().double() - y).abs()
+    assert (err <= tol * y.abs()).all(), float((err / y.abs()).max() * 2.0 ** 24)
+    # the slope sg (1 + z (1 - sg)): where z < -2 its two terms differ in size by z, no cancellation
+    z = x["gate"].double()
+    dy = torch.ones_like(x["x"])
+    got = G.gdr_rms_norm_bwd(d["x"], dy.cuda(), weight=d["weight"], gate=d["gate"])["dgate"].cpu().double()
+    h = x["x"].double()
+    sg = torch.sigmoid(z)
+    ref = h / (h.square().mean(-1, keepdim=True) + 1e-6).sqrt() * x["weight"].double() * sg * (1 + z * (1 - sg))
+    far = z < -4
+    assert ((got - ref).abs()[far] <= 2 * tol * ref.abs()[far]).all()
