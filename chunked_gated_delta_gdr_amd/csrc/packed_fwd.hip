@@ -34,6 +34,8 @@
 // bits.  The pairs need their values within fp16's range, so the wave keeps its columns under a
 // power-of-two scale F per column (the recurrence is linear in each value column), set anew for
 // every chunk: a pair is off by 2^-22 of the column's largest value.
+// A chunk with an infinity or a NaN in its keys, values, gains or decays goes token by token (by_token, in
+// the main wave, 0.8 us a token): what is not finite then reaches no earlier token and no other column.
 // Sums are fp32, the cumulative decay is summed in 64 bits and kept as two fp32 values (its differences
 // matter beside its size).
 #include <type_traits>
@@ -94,10 +96,11 @@ template <int ROW> __device__ __forceinline__ int swz(int i, int q) {
 
 // 2^n for n in the normal range
 __device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) << 23); }
+constexpr float kInf = __builtin_inff(), kNaN = __builtin_nanf("");
 // n with 2^n <= x < 2^(n + 1) (-127 below the normal range); kNone for zero, infinite and NaN
 constexpr int kNone = -1000;
 __device__ __forceinline__ int log2_floor(float x) {
-  return x > 0.f && x < __int_as_float(0x7f800000) ? static_cast<int>(__float_as_uint(x) >> 23) - 127 : kNone;
+  return x > 0.f && x < kInf ? static_cast<int>(__float_as_uint(x) >> 23) - 127 : kNone;
 }
 // the same within [-100, 100], 0 where there is none: for factors whose inverse is needed too
 __device__ __forceinline__ int log2_near(float x) {
@@ -281,7 +284,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
     const double x = scan64(lane < n ? la : 0.f);
     gh[lane] = static_cast<float>(x);
     gl[lane] = static_cast<float>(x - gh[lane]);
-    bt[lane] = lane < n ? b : 0.f;
+    bt[lane] = lane < n ? (la < kInf ? b : kNaN) : 0.f;
   }
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -312,8 +315,8 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
         ss = sum16(ss);
         const float eps = a.qk_eps * f * f;
         // (a row so far below eps that eps leaves the type on the row's scale: 2^-ex / sqrt(2^(-2 ex) eps) = 1 / sqrt(eps))
-        rest = eps < __int_as_float(0x7f800000) ? rsqrt_f(ss + eps) : rsqrt_f(a.qk_eps) * rest;
-        if (ss == 0.f && a.qk_eps == 0.f) rest = __int_as_float(0x7fc00000);   // 0 / 0
+        rest = eps < kInf ? rsqrt_f(ss + eps) : rsqrt_f(a.qk_eps) * rest;
+        if (ss == 0.f && a.qk_eps == 0.f) rest = kNaN;   // 0 / 0
       }
       typedef _Float16 hE __attribute__((ext_vector_type(E)));
       uint8_t *dst = (which == 0 ? Ks : Qs) + swz<ROW>(i, c0 / 8) + (c0 % 8) * 2;
@@ -327,6 +330,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
       }
       *reinterpret_cast<hE *>(dst) = y;
       if constexpr (NP == 2) *reinterpret_cast<hE *>(dst + PART) = z;
+      if (which == 0 && !(m < 0x1p100f)) rest = kNaN;   // (a mark, as the values' factor: see by_token)
       if ((tid & 15) == 0) {
         // (past the end rows of zeros stand in, whose norm without eps is 1 / 0: they weigh nothing)
         (which == 0 ? sk : su)[i] = i < n ? rest : 0.f;
@@ -439,7 +443,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
     if (g == 0) {
       const auto put = [&](int at, float x) { reinterpret_cast<float *>(rec + at)[i] = x; };
       const float tau = pow2(ex), eg = expf(gi), ec = expf((gh[kC - 1] - gi) + (gl[kC - 1] - gi_low));
-      put(Rec::bv, bt[i] * si * pow2(kLift));
+      put(Rec::bv, top < kInf ? bt[i] * si * pow2(kLift) : kNaN);
       put(Rec::bk, -bs * eg * pow2(kLift));
       put(Rec::dt, tau);
       put(Rec::dc, tau * ec);
@@ -479,7 +483,7 @@ template <typename IO, int DK, int MAIN> struct Lds {
   static constexpr int v_col = 68;                  // (columns 4 banks apart)
   static constexpr int stage = V + cols * v_col * 4;
   // a main wave's hand-over, twice: S by K block, E by K block, parts next to each other, as B operands;
-  // then the columns' factors: how far S was brought down since, and 1 / F
+  // then the columns' factors: how far S was brought down since, and 1 / F (0: the chunk is written already)
   static constexpr int E = NS * NE * 1024, scale = E + 2 * NE * 1024, hand = scale + 2 * 16 * 4;
   static constexpr int hands = 2 * MAIN * hand;
   // two stages where they fit beside each other: the next chunk is written during this one
@@ -658,7 +662,8 @@ template <typename IO, int DK> struct Output {
       }
     }
   }
-  __device__ __forceinline__ void values(const uint8_t *hand, int lane, const f4 *x, f4 *o) const {
+  // returns 1 / F
+  __device__ __forceinline__ float values(const uint8_t *hand, int lane, const f4 *x, f4 *o) const {
     f4 pe[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) pe[mt] = f4{0.f, 0.f, 0.f, 0.f};
@@ -684,6 +689,7 @@ template <typename IO, int DK> struct Output {
       const f4 u = kRowsAhead ? oq[kRowsAhead ? mt : 0] : row(Rec::oq, mt), w = kRowsAhead ? op[kRowsAhead ? mt : 0] : row(Rec::op, mt);
       o[mt] = (u * (x[mt] * down) + w * pe[mt]) * Finv;
     }
+    return Finv;
   }
 };
 
@@ -701,6 +707,79 @@ __device__ __forceinline__ float max_col(float m) {
   u = __float_as_uint(m);
   p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   return __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+__device__ __forceinline__ float sum_col(float x) {
+  uint32_t u = __float_as_uint(x);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  u = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// The rule token by token in fp32, for chunks that the pairs do not hold: n tokens from t0 on, S the
+// state's channels 16 t + 4 (lane / 16) + 0..3 of value column col.  Products by chunk would take what
+// is not finite to every token of it (0 * NaN in T's and P's zeros); here it reaches later ones only.
+template <typename IO, int DK, typename Args>
+__device__ __forceinline__ void by_token(const Args &a, f4 *S, int t0, int n, int h, int hk, int col, int lane) {
+  constexpr int NT = DK / 16;
+  const int g = lane >> 4;
+  const IO *kp = static_cast<const IO *>(a.k) + hk * a.Dk + 4 * g, *qp = static_cast<const IO *>(a.q) + hk * a.Dk + 4 * g;
+  const IO *vp = static_cast<const IO *>(a.v) + static_cast<long long>(h) * a.Dv + col;
+  IO *op = static_cast<IO *>(a.out) + static_cast<long long>(h) * a.Dv + col;
+  const bool colin = col < a.Dv;
+  typedef typename Vec<IO, 4>::type raw4;
+  raw4 kr[NT], qr[NT];   // the next token's, under way
+  IO vr = from_f<IO>(0.f);
+  float beta_r = 0.f, la_r = 0.f;
+  const auto load = [&](int t) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      kr[j] = qr[j] = raw4{};
+      if (16 * j + 4 * g < a.Dk) {
+        kr[j] = *reinterpret_cast<const raw4 *>(kp + t * a.ks + 16 * j);
+        qr[j] = *reinterpret_cast<const raw4 *>(qp + t * a.qs + 16 * j);
+      }
+    }
+    const long long at = static_cast<long long>(t) * a.Hv + h;
+    if (colin) vr = vp[t * a.vs];
+    beta_r = a.beta[at];
+    if (a.log_alpha != nullptr) la_r = a.log_alpha[at];
+  };
+  load(t0);
+#pragma unroll 1
+  for (int t = t0; t < t0 + n; ++t) {
+    f4 k[NT], q[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        k[j][e] = to_f(static_cast<IO>(kr[j][e]));
+        q[j][e] = to_f(static_cast<IO>(qr[j][e]));
+      }
+    const float v = to_f(vr), beta = beta_r, alpha = __expf(la_r);
+    if (t + 1 < t0 + n) load(t + 1);
+    const auto dot = [&](const f4 *x, const f4 *y) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = fmaf(x[j][e], y[j][e], s);
+      return sum_col(s);
+    };
+    if (a.qk_norm) {
+      const float fk = rsqrt_f(dot(k, k) + a.qk_eps), fq = rsqrt_f(dot(q, q) + a.qk_eps);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        k[j] *= fk;
+        q[j] *= fq;
+      }
+    }
+    const float d = beta * (v - alpha * dot(S, k)), o = a.scale * fmaf(d, dot(k, q), alpha * dot(S, q));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) S[j] = d * k[j] + alpha * S[j];
+    if (g == 0 && colin) op[t * a.os] = from_f<IO>(o);
+  }
 }
 
 // A chunk's A operands in the order of their use, kDepth of them under way from LDS: the reads take
@@ -808,11 +887,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     const auto finish = [&](int c) {
       f4 x[4], o[4];
       out.query(hand(w, c), lane, x);
-      out.values(hand(w, c), lane, x, o);
+      // (a chunk that the main wave has written: dropped)
+      const uint32_t o_here = out.values(hand(w, c), lane, x, o) == 0.f ? 0x80000000u : o_at;
       if (c + 1 < chunks) out.load(qp + (c + 1) * q_step, rec + (c + 1) * rec_step, lane);
       const Rows<IO> rows(op + (t0 + c * kC) * a.os, left(c), a.os, a.Dv);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) rows.put4(quad_transpose(o[mt], lane), o_at + 16 * mt * o_row);
+      for (int mt = 0; mt < 4; ++mt) rows.put4(quad_transpose(o[mt], lane), o_here + 16 * mt * o_row);
     };
     if (chunks > 0) out.load(qp, rec, lane);
     for (int c = 0; c < chunks; ++c) {
@@ -842,201 +922,228 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   constexpr std::integral_constant<int, 2> two{};
   constexpr std::integral_constant<int, 4> four{};
 
-  for (int c = 0; c < chunks; ++c) {
-    chunk_done<L::stages>(c);
-    __syncthreads();   // stage c is filled
-    const uint8_t *st = stage(c);
-    uint8_t *ho = hand(wave, c);
-    const auto rows = [&](int at, int mt) { return *reinterpret_cast<const f4 *>(st + L::rec + at + 4 * (16 * mt + 4 * g)); };
-    // k^ and k^T by K block and row tile, T between them; parts next to each other
-    constexpr int nK = 4 * NS * NP, nT = 2 * kFrags, nKT = 2 * NT * NP;
-    constexpr int iT = nK, iKT = iT + nT;
-    const auto at = [&](int i) -> const uint8_t * {
-      if (i < iT) return st + L::K + (i % NP) * L::part + swz<DK * 2>(16 * (i / NP % 4) + r, 4 * (i / NP / 4) + g);
-      if (i < iKT) return st + L::rec + Rec::T + (i - iT) % 2 * kFragBytes + ((i - iT) / 2 * 64 + lane) * 16;
-      return st + L::KT + ((i - iKT) % NP) * L::part + swz<128>(16 * ((i - iKT) / NP % NT) + r, 4 * ((i - iKT) / NP / NT) + g);
-    };
-    f4 v[4];
+  int c = 0;
+  while (true) {
+    for (; c < chunks; ++c) {
+      chunk_done<L::stages>(c);
+      __syncthreads();   // stage c is filled
+      const uint8_t *st = stage(c);
+      uint8_t *ho = hand(wave, c);
+      const auto rows = [&](int at, int mt) { return *reinterpret_cast<const f4 *>(st + L::rec + at + 4 * (16 * mt + 4 * g)); };
+      // k^ and k^T by K block and row tile, T between them; parts next to each other
+      constexpr int nK = 4 * NS * NP, nT = 2 * kFrags, nKT = 2 * NT * NP;
+      constexpr int iT = nK, iKT = iT + nT;
+      const auto at = [&](int i) -> const uint8_t * {
+        if (i < iT) return st + L::K + (i % NP) * L::part + swz<DK * 2>(16 * (i / NP % 4) + r, 4 * (i / NP / 4) + g);
+        if (i < iKT) return st + L::rec + Rec::T + (i - iT) % 2 * kFragBytes + ((i - iT) / 2 * 64 + lane) * 16;
+        return st + L::KT + ((i - iKT) % NP) * L::part + swz<128>(16 * ((i - iKT) / NP % NT) + r, 4 * ((i - iKT) / NP / NT) + g);
+      };
+      f4 v[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      v[mt] = *reinterpret_cast<const f4 *>(st + L::V + ((16 * wave + r) * L::v_col + 16 * mt + 4 * g) * 4);
-    Stream<kDepth, decltype(at)> ops(at, iKT + nKT);
-    // operands i, i + parts, .. times a pair, each onto its own accumulator (fresh: onto zeros),
-    // without the products of low parts
-    const auto pairs = [&](auto parts, auto n, int i, h8 bh, h8 bl, f4 *c, bool fresh, auto &&beside) {
-      constexpr int NPP = decltype(parts)::value, N = decltype(n)::value;
-      h8 ah[N], al[N];
+      for (int mt = 0; mt < 4; ++mt)
+        v[mt] = *reinterpret_cast<const f4 *>(st + L::V + ((16 * wave + r) * L::v_col + 16 * mt + 4 * g) * 4);
+      Stream<kDepth, decltype(at)> ops(at, iKT + nKT);
+      // operands i, i + parts, .. times a pair, each onto its own accumulator (fresh: onto zeros),
+      // without the products of low parts
+      const auto pairs = [&](auto parts, auto n, int i, h8 bh, h8 bl, f4 *c, bool fresh, auto &&beside) {
+        constexpr int NPP = decltype(parts)::value, N = decltype(n)::value;
+        h8 ah[N], al[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        ah[j] = ops.take(i + j * NPP);
-        if constexpr (NPP == 2) al[j] = ops.take(i + j * NPP + 1);
-      }
-      const f4 zero = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (NPP == 2) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) c[j] = mma(al[j], bh, fresh ? zero : c[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = mma(ah[j], bl, fresh && NPP == 1 ? zero : c[j]);
-#pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = mma(ah[j], bh, c[j]);
-      beside();   // other work, three instructions between two products
-#pragma unroll
-      for (int j = 0; j < N * (NPP + 1); ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    const auto give = [&](int at, int k, h8 hi, h8 lo) {   // to the output wave
-      *reinterpret_cast<h8 *>(ho + at + (k * L::NE * 64 + lane) * 16) = hi;
-      if constexpr (L::NE == 2) *reinterpret_cast<h8 *>(ho + at + ((2 * k + 1) * 64 + lane) * 16) = lo;
-    };
-
-    // the column's scale: the largest of its state and of bv V to [2^kTop, 2^(kTop + 1)).  The
-    // accumulators stay under the last chunk's scale, f behind, until they are updated.
-    float mv = 0.f, ms = 0.f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) mv = max4(mv, v[t]);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ms = max4(ms, acc[t]);
-    float f;
-    {
-      const int es = log2_floor(max_col(ms)), top = max(log2_floor(max_col(mv)), es == kNone ? kNone : es - kLift - lf);
-      int to = top == kNone ? lf : min(kMaxScale, max(-kMaxScale, kTop - top));
-      to = min(lf + 126, max(lf - 126, to));
-      f = pow2(to - lf);
-      lf = to;
-    }
-
-    // X = bv V + bk (k^ S^T)
-    f4 x[4];
-    h8 bh[NS], bl[NS];
-    const float down_s = f * pow2(-kLift);
-    const auto split_state = [&](int k) {
-      split8(acc[2 * k] * down_s, acc[2 * k + 1] * down_s, one, bh[k], bl[k]);
-      give(0, k, bh[k], bl[k]);
-    };
-    split_state(0);
-    __builtin_amdgcn_sched_barrier(0);
-    f4 rbk[4], rdt[4], rdc[4];   // row factors, read while the first products run
-    float ec = 0.f;
-#pragma unroll
-    for (int k = 0; k < NS; ++k)
-      pairs(parts, four, k * 4 * NP, bh[k], bl[k], x, k == 0, [&] {
-        if (k == 0) {
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) rbk[mt] = rows(Rec::bk, mt);
-          ec = *reinterpret_cast<const float *>(st + L::rec + Rec::ec) * f;
+        for (int j = 0; j < N; ++j) {
+          ah[j] = ops.take(i + j * NPP);
+          if constexpr (NPP == 2) al[j] = ops.take(i + j * NPP + 1);
         }
-        if (k + 1 < NS) split_state(k + 1);
-      });
-    {
-      const float F = pow2(lf);
+        const f4 zero = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (NPP == 2) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) x[mt] = rbk[mt] * x[mt] + v[mt] * F;
-    }
-    // E = T X, in halves of 32 rows: X's second half is split beside the products of the first, the
-    // state's decay and E's first half follow beside them
-    f4 d[4], ed[4];
-    float mx = 0.f, me = 0.f;   // largest of a column's X and E, of this lane's rows
-    h8 xh[2], xl[2], eh[2], el[2];
-    const auto split_x = [&](int k) { split8(x[2 * k], x[2 * k + 1], one, xh[k], xl[k]); };
-    const auto finish_e = [&](int k) {   // E's rows 32 k ..: as they are, and as the update takes them
+          for (int j = 0; j < N; ++j) c[j] = mma(al[j], bh, fresh ? zero : c[j]);
+        }
 #pragma unroll
-      for (int mt = 2 * k; mt < 2 * k + 2; ++mt) {
-        ed[mt] = rdt[mt] * d[mt];
-        me = max4(me, ed[mt]);
-      }
-    };
-    const auto split_e = [&](int k) { split8(rdc[2 * k] * d[2 * k], rdc[2 * k + 1] * d[2 * k + 1], one, eh[k], el[k]); };
-    const auto give_e = [&](int k) {
-      h8 oh, ol;
-      split8(ed[2 * k], ed[2 * k + 1], one, oh, ol);
-      give(L::E, k, oh, ol);
-    };
-    split_x(0);
-    __builtin_amdgcn_sched_barrier(0);
-    pairs(two, four, iT, xh[0], xl[0], d, true, [&] {
+        for (int j = 0; j < N; ++j) c[j] = mma(ah[j], bl, fresh && NPP == 1 ? zero : c[j]);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        rdt[mt] = rows(Rec::dt, mt);
-        rdc[mt] = rows(Rec::dc, mt);
-      }
-      split_x(1);
+        for (int j = 0; j < N; ++j) c[j] = mma(ah[j], bh, c[j]);
+        beside();   // other work, three instructions between two products
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] *= ec;
+        for (int j = 0; j < N * (NPP + 1); ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      const auto give = [&](int at, int k, h8 hi, h8 lo) {   // to the output wave
+        *reinterpret_cast<h8 *>(ho + at + (k * L::NE * 64 + lane) * 16) = hi;
+        if constexpr (L::NE == 2) *reinterpret_cast<h8 *>(ho + at + ((2 * k + 1) * 64 + lane) * 16) = lo;
+      };
+
+      // the column's scale: the largest of its state and of bv V to [2^kTop, 2^(kTop + 1)).  The
+      // accumulators stay under the last chunk's scale, f behind, until they are updated.
+      float mv = 0.f, ms = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) mx = max4(mx, x[mt]);
-    });
-    pairs(two, two, iT + 2 * 4, xh[1], xl[1], d + 2, false, [&] {
-      finish_e(0);
-      split_e(0);
-    });
-    finish_e(1);
-    float down = 1.f;
-    if (__builtin_expect(__any(!(__builtin_elementwise_maximum(mx, me) <= kOver)), false)) {
-      // past fp16's range: the columns are brought down, and E formed again
-#pragma unroll 1
-      for (int turn = 0; turn < 2; ++turn) {   // (where X did not fit, E says nothing yet)
-        mx = max_col(mx);
-        const int over = log2_floor(mx <= kOver ? max_col(me) : mx);
-        const int to = over == kNone ? lf : max(-kMaxScale, min(lf, lf + kTop - over));
-        const float now = pow2(to - lf);
+      for (int t = 0; t < 4; ++t) mv = max4(mv, v[t]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) ms = max4(ms, acc[t]);
+      mv = max_col(mv);
+      ms = max_col(ms);
+      // a value, or by its mark in bv a key, gain or decay, that is not finite (a state that is not has no
+      // token before it, and stays in its column)
+      const bool odd = !(mv < kInf);
+      float f;
+      int last;
+      {
+        const int es = log2_floor(ms), top = max(log2_floor(mv), es == kNone ? kNone : es - kLift - lf);
+        int to = top == kNone ? lf : min(kMaxScale, max(-kMaxScale, kTop - top));
+        to = min(lf + 126, max(lf - 126, to));
+        f = pow2(to - lf);
+        last = lf;
         lf = to;
-        down *= now;
-        mx = me = 0.f;
+      }
+
+      // X = bv V + bk (k^ S^T)
+      f4 x[4];
+      h8 bh[NS], bl[NS];
+      const float down_s = f * pow2(-kLift);
+      const auto split_state = [&](int k) {
+        split8(acc[2 * k] * down_s, acc[2 * k + 1] * down_s, one, bh[k], bl[k]);
+        give(0, k, bh[k], bl[k]);
+      };
+      split_state(0);
+      __builtin_amdgcn_sched_barrier(0);
+      f4 rbk[4], rdt[4], rdc[4];   // row factors, read while the first products run
+      float ec = 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] *= now;
+      for (int k = 0; k < NS; ++k)
+        pairs(parts, four, k * 4 * NP, bh[k], bl[k], x, k == 0, [&] {
+          if (k == 0) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) rbk[mt] = rows(Rec::bk, mt);
+            ec = *reinterpret_cast<const float *>(st + L::rec + Rec::ec) * f;
+          }
+          if (k + 1 < NS) split_state(k + 1);
+        });
+      {
+        const float F = pow2(lf);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) x[mt] = rbk[mt] * x[mt] + v[mt] * F;
+      }
+      // not for the pairs (decided here, where the answer is there without a wait; the state is as it was)
+      if (__builtin_expect(__any(odd), false)) {
+        lf = last;
+        break;
+      }
+      // E = T X, in halves of 32 rows: X's second half is split beside the products of the first, the
+      // state's decay and E's first half follow beside them
+      f4 d[4], ed[4];
+      float mx = 0.f, me = 0.f;   // largest of a column's X and E, of this lane's rows
+      h8 xh[2], xl[2], eh[2], el[2];
+      const auto split_x = [&](int k) { split8(x[2 * k], x[2 * k + 1], one, xh[k], xl[k]); };
+      const auto finish_e = [&](int k) {   // E's rows 32 k ..: as they are, and as the update takes them
+#pragma unroll
+        for (int mt = 2 * k; mt < 2 * k + 2; ++mt) {
+          ed[mt] = rdt[mt] * d[mt];
+          me = max4(me, ed[mt]);
+        }
+      };
+      const auto split_e = [&](int k) { split8(rdc[2 * k] * d[2 * k], rdc[2 * k + 1] * d[2 * k + 1], one, eh[k], el[k]); };
+      const auto give_e = [&](int k) {
+        h8 oh, ol;
+        split8(ed[2 * k], ed[2 * k + 1], one, oh, ol);
+        give(L::E, k, oh, ol);
+      };
+      split_x(0);
+      __builtin_amdgcn_sched_barrier(0);
+      pairs(two, four, iT, xh[0], xl[0], d, true, [&] {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          x[mt] *= now;
-          mx = max4(mx, x[mt]);
+          rdt[mt] = rows(Rec::dt, mt);
+          rdc[mt] = rows(Rec::dc, mt);
         }
-        split_x(0);
         split_x(1);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          d[mt] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NT; ++t) acc[t] *= ec;
 #pragma unroll
-          for (int k = 0; k <= mt / 2; ++k) {
-            const uint8_t *p = at(iT + 2 * frag_of(mt, k));
-            const h8 th = *reinterpret_cast<const h8 *>(p), tl = *reinterpret_cast<const h8 *>(p + kFragBytes);
-            d[mt] = mma(tl, xh[k], d[mt]);
-            d[mt] = mma(th, xl[k], d[mt]);
-            d[mt] = mma(th, xh[k], d[mt]);
-          }
-        }
+        for (int mt = 0; mt < 4; ++mt) mx = max4(mx, x[mt]);
+      });
+      pairs(two, two, iT + 2 * 4, xh[1], xl[1], d + 2, false, [&] {
         finish_e(0);
-        finish_e(1);
-        if (!__any(!(__builtin_elementwise_maximum(mx, me) <= kOver))) break;
+        split_e(0);
+      });
+      finish_e(1);
+      float down = 1.f;
+      if (__builtin_expect(__any(mx > kOver || me > kOver), false)) {
+        // past fp16's range: the columns are brought down, and E formed again
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {   // (where X did not fit, E says nothing yet)
+          mx = max_col(mx);
+          const int over = log2_floor(mx <= kOver ? max_col(me) : mx);
+          const int to = over == kNone ? lf : max(-kMaxScale, min(lf, lf + kTop - over));
+          const float now = pow2(to - lf);
+          lf = to;
+          down *= now;
+          mx = me = 0.f;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[t] *= now;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            x[mt] *= now;
+            mx = max4(mx, x[mt]);
+          }
+          split_x(0);
+          split_x(1);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            d[mt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k <= mt / 2; ++k) {
+              const uint8_t *p = at(iT + 2 * frag_of(mt, k));
+              const h8 th = *reinterpret_cast<const h8 *>(p), tl = *reinterpret_cast<const h8 *>(p + kFragBytes);
+              d[mt] = mma(tl, xh[k], d[mt]);
+              d[mt] = mma(th, xl[k], d[mt]);
+              d[mt] = mma(th, xh[k], d[mt]);
+            }
+          }
+          finish_e(0);
+          finish_e(1);
+          if (!__any(mx > kOver || me > kOver)) break;
+        }
+        split_e(0);
       }
-      split_e(0);
-    }
-    // S <- e^{g_C} S + (e^{g_C - g} E)^T k^; beside the products E's second half, then its parts for
-    // the output wave
-    __builtin_amdgcn_sched_barrier(0);
+      // S <- e^{g_C} S + (e^{g_C - g} E)^T k^; beside the products E's second half, then its parts for
+      // the output wave
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int t = 0; t < NT; t += 4)
-        pairs(parts, four, iKT + (k * NT + t) * NP, eh[k], el[k], acc + t, false, [&] {
-          if (k == 0 && t == 0) split_e(1);
-          if (t + 4 == NT) give_e(k);
-        });
-    if (g == 0) {
-      float *scale = reinterpret_cast<float *>(ho + L::scale) + r;
-      scale[0] = down;
-      scale[16] = pow2(-lf);
+        for (int t = 0; t < NT; t += 4)
+          pairs(parts, four, iKT + (k * NT + t) * NP, eh[k], el[k], acc + t, false, [&] {
+            if (k == 0 && t == 0) split_e(1);
+            if (t + 4 == NT) give_e(k);
+          });
+      if (g == 0) {
+        float *scale = reinterpret_cast<float *>(ho + L::scale) + r;
+        scale[0] = down;
+        scale[16] = pow2(-lf);
+      }
     }
+    if (c >= chunks) break;
+    // (what the other path needs is formed here, not kept over the loop)
+    int here = lane;
+    asm volatile("" : "+v"(here));
+    typedef __attribute__((address_space(4))) const PackedArgs *Args;
+    Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] *= pow2(-kLift - lf);
+    by_token<IO, DK>(*args, acc, t0 + c * kC, left(c), h, hk, col, here);
+    lf = -kLift;
+    if (here < 16) reinterpret_cast<float *>(hand(wave, c) + L::scale)[16 + here] = 0.f;
+    ++c;
   }
   __syncthreads();
   if (pooled && colin) {
-    const float Finv = pow2(-lf);
+    const float f = pow2(-kLift - lf);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      acc[t] *= pow2(-kLift);
-      const float x[4] = {acc[t][0] * Finv, acc[t][1] * Finv, acc[t][2] * Finv, acc[t][3] * Finv};
+      const float x[4] = {acc[t][0] * f, acc[t][1] * f, acc[t][2] * f, acc[t][3] * f};
       if (16 * t + 4 * g < a.Dk) store_n<4>(S + 16 * t + 4 * g, x);
     }
   }

@@ -356,7 +356,9 @@ int gdr_chunk_fwd_impl(const gdr_desc_t *desc);
  *    graph may be replayed on other values).  cu_seqlens must not decrease; values outside
  *    [0, n_tokens] are clamped into it, so a bad one gives wrong rows but touches no other
  *    memory.  Rows of no sequence are left as they were.
- *  - q, k, v and gates that are NaN or infinite stay within their sequence and value heads.
+ *  - NaN and infinities stay within their sequence and value heads and reach no earlier token; those
+ *    of v and of a state's row stay in that value channel (but for the output norm, which joins a
+ *    row's channels), those of q in that token's rows.
  *  - log_alpha <= 0; -inf (a reset) is exact: decays below exp(-200) per token are zero in fp32.
  * ------------------------------------------------------------------------------------------ */
 enum { GDR_F16 = 2 };   /* io_dtype: the packed and norm entry points also take fp16 */

@@ -131,3 +131,40 @@ def test_tiny_keys_under_the_norm(entry, io, size):
     assert R.rel(pool, ref_p) <= R.state_tol(70)
     if size >= 1e-12:   # (beyond, the output's own products leave fp32's range or io's)
         assert R.rel(out, ref_o) <= io_tol(x, entry) + R.state_tol(70)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "log_alpha", "pool"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [0, 20, 63, 64, 69])
+def test_what_is_not_finite_reaches_no_earlier_token(entry, io, name, bad, at):
+    """The tokens in front keep their values, and of a bad value or state row the other value channels."""
+    import torch
+    if name == "log_alpha" and bad > 0:
+        pytest.skip("log_alpha <= 0")
+    x = R.make([70, 5], Hk=2, Hv=4, Dk=64, Dv=64, io=io, seed=94)
+    ref_o, ref_p = R.delta(x, torch.zeros(x["v"].shape))
+    y = dict(x, **{name: x[name].clone()})
+    if name == "pool":
+        y["pool"][0, 1, 3, 5] = bad
+    elif name == "v":
+        y["v"][at, 1, 3] = bad
+    else:
+        y[name][at, 0] = bad
+    out, pool = run(y, entry)
+    tol = io_tol(x, entry) + R.state_tol(70)
+    if name != "pool" and at > 0:
+        assert R.rel(out[:at], ref_o[:at]) <= tol
+    assert R.rel(out[70:], ref_o[70:]) <= tol and R.rel(out[:, 2:], ref_o[:, 2:]) <= tol
+    assert R.rel(pool[1], ref_p[1]) <= R.state_tol(70) and R.rel(pool[:, 2:], ref_p[:, 2:]) <= R.state_tol(70)
+    if name in ("v", "pool"):
+        rest = [c for c in range(64) if c != 3]
+        assert R.rel(out[:, :, rest], ref_o[:, :, rest]) <= tol
+        assert R.rel(pool[:, :, rest], ref_p[:, :, rest]) <= R.state_tol(70)
+        assert not torch.isfinite(out[at if name == "v" else 0:70, 1, 3].float()).any()
+    elif name == "q":
+        rest = [i for i in range(75) if i != at]
+        assert R.rel(out[rest], ref_o[rest]) <= tol and R.rel(pool, ref_p) <= R.state_tol(70)
+    else:
+        assert not torch.isfinite(out[at:70, 0].float()).all() and not torch.isfinite(pool[0, 0]).all()
