@@ -34,8 +34,11 @@
 // bits.  The pairs need their values within fp16's range, so the wave keeps its columns under a
 // power-of-two scale F per column (the recurrence is linear in each value column), set anew for
 // every chunk: a pair is off by 2^-22 of the column's largest value.
-// A chunk with an infinity or a NaN in its keys, values, gains or decays goes token by token (by_token, in
-// the main wave, 0.8 us a token): what is not finite then reaches no earlier token and no other column.
+// Where sizes in a column differ so much that this would show (a reset of a large state, one value far above
+// the others), the chunk goes token by token in fp32 (by_token, in the main wave, 0.8 us a token); kFar below
+// says when.  Asking costs 1 % under decays of e^-5 a chunk, 5 % under e^-10, 15 % under e^-100 (4 x 4096
+// tokens, a call: 215, 220 and 245 us; 213 unasked).
+// So does a chunk with an infinity or a NaN in its keys, values, gains or decays: what is not finite then reaches no earlier token and no other column.
 // Sums are fp32, the cumulative decay is summed in 64 bits and kept as two fp32 values (its differences
 // matter beside its size).
 #include <type_traits>
@@ -71,7 +74,8 @@ template <bool kPair> struct Record {
   static constexpr int T = 0;                                  // hi, lo
   // row factors [64] fp32 of the state's waves: of k^ S^T in X, of T's rows in E and in the update
   static constexpr int bk = 2 * kFragBytes, dt = bk + kC * 4, dc = dt + kC * 4;
-  static constexpr int ec = dc + kC * 4;                       // e^{g_C}
+  static constexpr int ec = dc + kC * 4;                       // e^{g_C}; how far below M a state may be to hold a size
+                                                               // of 2^-kNear M (an exponent); the strongest decay
   static constexpr int staged = ec + 16;                       // what comes before goes to LDS
   // and of the others: V in X, q^ S^T and P E in O, and the factor of k^ = kf k
   static constexpr int bv = staged, oq = bv + kC * 4, op = oq + kC * 4, kf = op + kC * 4;
@@ -119,6 +123,21 @@ constexpr int kTop = 9, kKeyTop = 7, kQueryTop = 3, kPShift = 5, kLift = 9;
 constexpr int kDepth = 12;   // operands under way from LDS (at most 15 reads are counted)
 constexpr int kMaxScale = 110;
 constexpr float kOver = 32768.f;
+
+// What one scale for a column's 64 tokens and state costs.  With M the largest of them, fp16's smallest
+// step leaves X, E, S and T's products off by 2^-34 M, and P's products with E by 2^-30 of the largest up
+// to the row; a state or rows whose own size has fallen far below M, by a reset or strong decays or
+// because M comes later, would lose their bits to that.  So the sizes are followed through the chunk,
+//     A_i = max(alpha_i A_{i-1}, |bv_i V_i|)   from A_-1 = |S|   (the rule's, without what it erases).
+// Far is A_63 < 2^-14 M (else states are good to 2^-20, beside fp32's own roundings of a chunk), and A_i < 2^-kFar M
+// or < 2^-kFarBefore of the largest up to i (else rows to 2^-12 in bf16, as the output's one-part factors, 2^-13
+// in fp16 and 2^-18 in fp32).  The chunk goes token by token where two rows running are far in a column, or
+// where a column's M makes a row far as measured by the row's largest of 16 columns (one small value among
+// its neighbours, of which random data always has some, is neither).
+constexpr int kFarEnd = 14;
+template <typename IO> constexpr int kFar = sizeof(IO) == 4 ? 16 : kExact<IO> ? 21 : 22;
+template <typename IO> constexpr int kFarBefore = sizeof(IO) == 4 ? 12 : kExact<IO> ? 17 : 18;
+template <typename IO> constexpr int kNear = kFarEnd < kFarBefore<IO> ? kFarEnd : kFarBefore<IO>;   // near enough for all three
 
 // hi + lo = x to 22 bits, for two values: one conversion and two mixed-precision multiply-adds.  x and
 // hi are made opaque: were the product behind x contracted into hi's conversion in one place and
@@ -222,6 +241,18 @@ __device__ __forceinline__ double scan64(double x) {
   return dpp_add<0x143, 0xc>(x);   // rows 2 and 3 from the end of row 1
 }
 
+// over the four lanes of a column: swapping the register with itself puts each lane next to its
+// neighbour 16 (32) lanes on (a shuffle through LDS takes 150 cycles, this a few)
+__device__ __forceinline__ float max_col(float m) {
+  uint32_t u = __float_as_uint(m);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  m = __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  u = __float_as_uint(m);
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float min_col(float m) { return -max_col(-m); }
+
 // LDS: k^ and q^ are dead once M and P are formed, L and T take their place (four workgroups a CU
 // for 16-bit types, which hides the loads and the inverse's chain of small products).
 template <typename IO, int DK> struct PrepLds {
@@ -276,6 +307,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
     rows[0][p] = *reinterpret_cast<const raw *>(kp + (i * static_cast<uint32_t>(a.ks) + (chan ? c0 : 0)));
     rows[1][p] = *reinterpret_cast<const raw *>(qp + (i * static_cast<uint32_t>(a.qs) + (chan ? c0 : 0)));
   }
+  float drop = 0.f;   // (wave 0) the strongest log decay
   if (wave == 0) {   // cumulative log decay and the gains; tokens past the end change nothing
     const long long at = static_cast<long long>(t0 + min(lane, n - 1)) * a.Hv + h;
     float la = a.log_alpha != nullptr ? a.log_alpha[at] : 0.f;
@@ -285,6 +317,11 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
     gh[lane] = static_cast<float>(x);
     gl[lane] = static_cast<float>(x - gh[lane]);
     bt[lane] = lane < n ? (la < kInf ? b : kNaN) : 0.f;
+    drop = fminf(lane < n ? la : 0.f, 0.f);
+    drop = fminf(drop, dpp<0x128>(drop));
+    drop = fminf(drop, dpp<0x124>(drop));
+    drop = fminf(drop, dpp<0x122>(drop));
+    drop = min_col(fminf(drop, dpp<0x121>(drop)));
   }
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -385,6 +422,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
       }
   }
   __syncthreads();   // k^ and q^ are read
+  if (tid == 0) Tm[0][64] = __expf(drop);   // (beside T: its rows are padded)
   const float gi = gh[i], gi_low = gl[i];
   const float si = sk[i], bs = bt[i] * si * si;
 #pragma unroll
@@ -449,7 +487,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
       put(Rec::dc, tau * ec);
       put(Rec::oq, a.scale * su[i] * eg);
       put(Rec::op, a.scale * su[i] * pow2(kPShift - kLift));
-      if (i == kC - 1) *reinterpret_cast<float *>(rec + Rec::ec) = eg;
+      if (i == kC - 1) *reinterpret_cast<f4 *>(rec + Rec::ec) = f4{eg, __int_as_float(kNear<IO> - 1 - static_cast<int>(ceilf(-1.442695f * gi))), Tm[0][64], 0.f};
     }
   }
 }
@@ -698,23 +736,89 @@ __device__ __forceinline__ float max4(float m, f4 x) {
   m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(x[0])), fabsf(x[1]));
   return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(x[2])), fabsf(x[3]));
 }
-// over the four lanes of a column: swapping the register with itself puts each lane next to its
-// neighbour 16 (32) lanes on (a shuffle through LDS takes 150 cycles, this a few)
-__device__ __forceinline__ float max_col(float m) {
-  uint32_t u = __float_as_uint(m);
-  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  m = __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
-  u = __float_as_uint(m);
-  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
-}
-
 __device__ __forceinline__ float sum_col(float x) {
   uint32_t u = __float_as_uint(x);
   auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   u = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
   p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Whether no size falls too far below the column's M, looked at closer: its state holds it up alone, or each
+// pair of rows has one that carries the next pair (with the state, for the first), or each row holds its own;
+// rows from n on left out.  v: the column's 64 values bv V; s: its state's size; decay: the chunk's; decay3: no
+// decay over three tokens is below it.
+template <typename IO>
+__device__ __forceinline__ bool clearly_near(const float *v, float s, float M, float decay, float decay3, int n, int g) {
+  float pairs = kInf, each = kInf, last = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f4 x = *reinterpret_cast<const f4 *>(v + 16 * g + 4 * j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * g + 4 * j + e;   // (rows from n on: as if there were none)
+      if ((e & 1) == 0) pairs = i < n ? fminf(pairs, fmaxf(fmaxf(fabsf(x[e]), fabsf(x[e + 1])), i == 0 ? s : 0.f)) : pairs;
+      each = i < n ? fminf(each, fabsf(x[e])) : each;
+      last = i == n - 1 ? fabsf(x[e]) : last;
+      if (j == 0 && e == 0) pairs = g == 0 ? fminf(pairs, fmaxf(fabsf(x[0]), s)) : pairs;
+    }
+  }
+  pairs = min_col(pairs);
+  each = min_col(each);
+  last = max_col(last);
+  return !(pairs * decay3 < M * pow2(-kNear<IO>)) || !(each < M * pow2(-kFarBefore<IO>) || last < M * pow2(-kFarEnd)) ||
+         !(s * decay < M * pow2(-kNear<IO>));
+}
+
+// Whether the chunk is far, from the sizes themselves: each lane follows 16 rows from nothing, then from what
+// the lanes before leave.
+template <typename IO, typename Args>
+__device__ __forceinline__ bool falls_far(const Args &a, const float *v, float s, float M, int t0, int n, int h, int lane) {
+  const int g = lane >> 4;
+  float x[16], al[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int i = 16 * g + j;
+    x[j] = fabsf(v[i]);
+    al[j] = a.log_alpha != nullptr && i < n ? a.log_alpha[static_cast<long long>(t0 + i) * a.Hv + h] : 0.f;
+  }
+  float A = 0.f, P = 1.f, m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    al[j] = __expf(al[j]);
+    A = fmaxf(A * al[j], x[j]);
+    P *= al[j];
+    m = fmaxf(m, x[j]);
+  }
+  float size = s, most = s;
+#pragma unroll
+  for (int b = 0; b < 3; ++b) {
+    const int from = (lane & 15) + 16 * b;
+    const float Ab = __shfl(A, from, 64), Pb = __shfl(P, from, 64), mb = __shfl(m, from, 64);
+    if (b < g) {
+      size = fmaxf(size * Pb, Ab);
+      most = fmaxf(most, mb);
+    }
+  }
+  const auto far_below = [&](float a, float end) {   // (0: nothing there to lose)
+    return a > 0.f && (a < M * pow2(-kFar<IO>) || a < most * pow2(-kFarBefore<IO>) || a < end);
+  };
+  bool far = false, before = far_below(size, 0.f);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    size = fmaxf(size * al[j], x[j]);
+    most = fmaxf(most, x[j]);
+    float row = fmaxf(size, dpp<0x128>(size));
+    row = fmaxf(row, dpp<0x124>(row));
+    row = fmaxf(row, dpp<0x122>(row));
+    row = fmaxf(row, dpp<0x121>(row));
+    const float end = j == 15 && g == 3 ? M * pow2(-kFarEnd) : 0.f;
+    const bool here = far_below(size, end);
+    far |= (here && before) || far_below(row, end);
+    before = here;
+    if (j == 14 && g == 3) before |= far_below(size, M * pow2(-kFarEnd));
+  }
+  return far;
 }
 
 // The rule token by token in fp32, for chunks that the pairs do not hold: n tokens from t0 on, S the
@@ -803,6 +907,14 @@ template <int kDepth, typename At> struct Stream {
     return x;
   }
 };
+
+// The kernel's (only) argument, read again where it is used instead of held in registers.
+__device__ __forceinline__ auto kernel_args() {
+  typedef __attribute__((address_space(4))) const PackedArgs *Args;
+  Args a = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(a));
+  return a;
+}
 
 template <typename IO, int DK, int MAIN>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void seq_kernel(PackedArgs a) {
@@ -923,10 +1035,15 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   constexpr std::integral_constant<int, 4> four{};
 
   int c = 0;
+  bool checked = false;   // chunk c is known to hold in the pairs
   while (true) {
+    float s0, M;
+    bool bad = false;   // what is not finite
     for (; c < chunks; ++c) {
-      chunk_done<L::stages>(c);
-      __syncthreads();   // stage c is filled
+      if (!checked) {
+        chunk_done<L::stages>(c);
+        __syncthreads();   // stage c is filled
+      }
       const uint8_t *st = stage(c);
       uint8_t *ho = hand(wave, c);
       const auto rows = [&](int at, int mt) { return *reinterpret_cast<const f4 *>(st + L::rec + at + 4 * (16 * mt + 4 * g)); };
@@ -988,9 +1105,10 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
       // token before it, and stays in its column)
       const bool odd = !(mv < kInf);
       float f;
-      int last;
+      int last, below;   // below: the state's exponent below the column's
       {
-        const int es = log2_floor(ms), top = max(log2_floor(mv), es == kNone ? kNone : es - kLift - lf);
+        const int es = log2_floor(ms), own = es == kNone ? kNone : es - kLift - lf, top = max(log2_floor(mv), own);
+        below = top - own;
         int to = top == kNone ? lf : min(kMaxScale, max(-kMaxScale, kTop - top));
         to = min(lf + 126, max(lf - 126, to));
         f = pow2(to - lf);
@@ -1010,25 +1128,59 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
       __builtin_amdgcn_sched_barrier(0);
       f4 rbk[4], rdt[4], rdc[4];   // row factors, read while the first products run
       float ec = 0.f;
+      int held = 0;
+      bool ask = false;
 #pragma unroll
       for (int k = 0; k < NS; ++k)
         pairs(parts, four, k * 4 * NP, bh[k], bl[k], x, k == 0, [&] {
           if (k == 0) {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) rbk[mt] = rows(Rec::bk, mt);
-            ec = *reinterpret_cast<const float *>(st + L::rec + Rec::ec) * f;
+            const float2 e = *reinterpret_cast<const float2 *>(st + L::rec + Rec::ec);
+            ec = e.x * f;
+            held = __float_as_int(e.y);
           }
           if (k + 1 < NS) split_state(k + 1);
+          // (most chunks under weak decays are held up by each column's state alone)
+          if (k + 1 == NS) ask = odd || below > held;
         });
+      // not for the pairs?  (Asked here, where the answer is there without a wait; the state is as it was.)
+      if (__builtin_expect(__any(ask), false) && !checked) {
+        s0 = ms * pow2(-kLift - last);
+        M = __builtin_elementwise_maximum(mv, s0);
+        const f4 words = *reinterpret_cast<const f4 *>(st + L::rec + Rec::ec);
+        const float decay = words[0], d1 = words[2], d3 = d1 * d1 * d1;   // (no three tokens decay by more than d3)
+        // Is a size far below M out of the question?  Every four rows have one that carries the next four, or
+        // every row holds its own, or the one before holds it up.  (Comparisons that NaN passes.)
+        float low = kInf, each = kInf, end = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          low = fminf(low, max4(0.f, v[t]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            end = e == 0 ? fabsf(v[t][0]) : fmaxf(fabsf(v[t][e]), fabsf(v[t][e - 1]) * d1);
+            each = fminf(each, end);
+          }
+        }
+        low = g == 0 ? fminf(low, fmaxf(fabsf(v[0][0]), s0)) : low;
+        each = g == 3 ? fminf(each, end * pow2(kFarEnd - kFarBefore<IO>)) : each;
+        bad = __any(odd);
+        if (bad || (__any(low * (d3 * d3 * d1) < M * pow2(-kNear<IO>)) && __any(each < M * pow2(-kFarBefore<IO>)))) {
+          int here = lane;
+          asm volatile("" : "+v"(here));
+          const float *column = reinterpret_cast<const float *>(st + L::V) + (16 * wave + (here & 15)) * L::v_col;
+          const bool near = clearly_near<IO>(column, s0, M, decay, d3, left(c), here >> 4);
+          if (bad || __any(!near)) {
+            lf = last;
+            break;
+          }
+        }
+      }
+      checked = false;
       {
         const float F = pow2(lf);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) x[mt] = rbk[mt] * x[mt] + v[mt] * F;
-      }
-      // not for the pairs (decided here, where the answer is there without a wait; the state is as it was)
-      if (__builtin_expect(__any(odd), false)) {
-        lf = last;
-        break;
       }
       // E = T X, in halves of 32 rows: X's second half is split beside the products of the first, the
       // state's decay and E's first half follow beside them
@@ -1128,12 +1280,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     // (what the other path needs is formed here, not kept over the loop)
     int here = lane;
     asm volatile("" : "+v"(here));
-    typedef __attribute__((address_space(4))) const PackedArgs *Args;
-    Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(args));
+    if (!bad) {
+      const float *column = reinterpret_cast<const float *>(stage(c) + L::V) + (16 * wave + (here & 15)) * L::v_col;
+      checked = !__any(falls_far<IO>(*kernel_args(), column, s0, M, t0 + c * kC, left(c), h, here));
+      if (checked) continue;
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] *= pow2(-kLift - lf);
-    by_token<IO, DK>(*args, acc, t0 + c * kC, left(c), h, hk, col, here);
+    by_token<IO, DK>(*kernel_args(), acc, t0 + c * kC, left(c), h, hk, col, here);
     lf = -kLift;
     if (here < 16) reinterpret_cast<float *>(hand(wave, c) + L::scale)[16 + here] = 0.f;
     ++c;

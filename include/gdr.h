@@ -399,7 +399,10 @@ typedef struct gdr_packed_inputs {
  *
  * Chunk form as gdr_chunk_fwd's.  The chunked kernel holds every product of the state's path to
  * about 22 bits (fp16 pairs under power-of-two scales, fp32 accumulation), so the states are as
- * exact as fp32 arithmetic makes them, in every io_dtype.
+ * exact as fp32 arithmetic makes them, in every io_dtype.  Where a value channel's sizes within a
+ * chunk differ by more than the pairs hold (a large state or value that a reset or strong decays
+ * take away, or that comes later), the chunk runs token by token: states stay within 2^-20 of
+ * their size beside fp32's own roundings, rows of out within their type's.
  *
  *   pool       [n_slots, Hv, Dv, Dk] fp32, read and written; NULL (n_slots = 0): every sequence
  *              starts from zeros and the final states are not kept.

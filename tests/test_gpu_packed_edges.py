@@ -168,3 +168,121 @@ def test_what_is_not_finite_reaches_no_earlier_token(entry, io, name, bad, at):
         assert R.rel(out[rest], ref_o[rest]) <= tol and R.rel(pool, ref_p) <= R.state_tol(70)
     else:
         assert not torch.isfinite(out[at:70, 0].float()).all() and not torch.isfinite(pool[0, 0]).all()
+
+
+def decays(x):
+    """How far the decays of a sequence may be off: e^x takes x with a rounding of 2^-24 of itself."""
+    la = x["log_alpha"].double()
+    return 2.0 ** -24 * float((-la).clamp(max=100).sum(0).max())
+
+
+def row_sizes(x):
+    """Of every token and head, the size that its output S q has where q is as far from S's large directions as
+    a random one: |S| scale / sqrt(Dv), in 64 bits."""
+    import math
+    import torch
+    k, v = x["k"].double(), x["v"].double()
+    k = k.repeat_interleave(v.shape[1] // k.shape[1], 1)
+    sizes, t = torch.zeros(v.shape[:2], dtype=torch.float64), 0
+    for s, n in enumerate(x["lens"]):
+        S = x["pool"][s].double() * (1.0 if x["has"] is None else float(x["has"][s]))
+        for i in range(t, t + n):
+            S = S * x["log_alpha"][i].double().exp()[:, None, None]
+            d = x["beta"][i].double()[:, None] * (v[i] - torch.matmul(S, k[i][:, :, None])[..., 0])
+            S = S + d[:, :, None] * k[i][:, None, :]
+            sizes[i] = S.square().sum((1, 2)).sqrt() * x["scale"] / math.sqrt(v.shape[2])
+        t += n
+    return sizes
+
+
+def check_rows(x, entry, rows, out, ref):
+    """Every row and head by itself.  A row is S q with a unit q: a relative error e of the products' factors leaves
+    e |S| |q| at most (Cauchy-Schwarz), which is row_sizes, however small the row is by q's direction.  e: a
+    rounding of 2^-12 for each of the three one-part factors of a bf16 output (2^-11, adding like their root);
+    four state tolerances, one for S and three for the products; each decay's own rounding."""
+    import torch
+    err = (out.double() - ref).square().mean(-1).sqrt()[rows]
+    part = 2.0 ** -11 if entry == "mfma" and x["v"].dtype == torch.bfloat16 else 0.0
+    tol = R.half_step(x["v"].dtype) * ref.square().mean(-1).sqrt() + (part + 4 * R.state_tol(max(x["lens"])) + decays(x)) * row_sizes(x)
+    assert (err <= tol[rows]).all(), float((err / tol[rows]).max())
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("big", [1e4, 1e6, 1e8, 1e12, 1e20])
+@pytest.mark.parametrize("what", ["state", "value"])
+@pytest.mark.parametrize("how", ["reset", "decays"])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 40)], ids=str)
+def test_what_decays_leaves_no_trace(entry, io, big, what, how, dims):
+    """A state or a value far larger than the rest, gone again within its chunk: what follows is
+    as exact as it is without."""
+    if io == "f16" and what == "value" and big > 1e4:
+        pytest.skip("beyond fp16")
+    x = R.make([70, 2, 64], Dk=dims[0], Dv=dims[1], io=io, seed=91)
+    if what == "state":
+        x["pool"] = x["pool"] * big
+    else:
+        x["v"][[7, 79]] = (x["v"][[7, 79]].double() * big).to(x["v"].dtype)
+    import math
+    for start in (0, 72):
+        if how == "reset":
+            x["log_alpha"][start + 20] = float("-inf")
+        else:
+            x["log_alpha"][start + 10:start + 26] = -1.25 * math.log(big) / 16
+    import torch
+    out, pool = run(x, entry)
+    ref_o, ref_p = R.delta(x, torch.zeros(x["v"].shape))
+    for s in (0, 2):
+        assert R.rel(pool[s], ref_p[s]) <= R.state_tol(70) + decays(x)
+    rows = torch.ones(136, dtype=torch.bool)
+    if io == "f16":   # (rows that fp16 does not hold)
+        rows = (ref_o.abs().amax((1, 2)) < 6e4)
+    check_rows(x, entry, rows, out, ref_o)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("big", [1e4, 1e6, 1e9, 1e15])
+@pytest.mark.parametrize("has", [False, True])
+def test_what_comes_later_leaves_no_trace(entry, io, big, has):
+    """A large value costs the tokens before it nothing."""
+    import torch
+    if io == "f16" and big > 1e4:
+        pytest.skip("beyond fp16")
+    x = R.make([70, 2, 64], Dk=64, Dv=64, io=io, has=[has] * 3, seed=92)
+    x["v"][[40, 100]] = (x["v"][[40, 100]].double() * big).to(x["v"].dtype)
+    out, pool = run(x, entry)
+    ref_o, ref_p = R.delta(x, torch.zeros(x["v"].shape))
+    assert R.rel(pool, ref_p) <= R.state_tol(70)
+    check_rows(x, entry, [i for i in range(136) if i < 40 or 70 <= i < 100], out, ref_o)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("step", [-0.05, -0.3, -1.0, -3.0, -20.0])
+def test_decays_of_every_size(entry, io, step):
+    """Values alike in size under weak to strong decays, some heads with each."""
+    import torch
+    x = R.make([200, 64, 1, 65], Hk=2, Hv=4, Dk=64, Dv=64, io=io, seed=93)
+    x["log_alpha"] = (x["log_alpha"] * 0 + step) * torch.rand(x["log_alpha"].shape, generator=torch.Generator().manual_seed(5)) * 2
+    x["log_alpha"][:, 1] = 0.0
+    out, pool = run(x, entry)
+    ref_o, ref_p = R.delta(x, torch.zeros(x["v"].shape))
+    # (each token's decay is a rounding of 2^-24 of its exponent; what is older than a few tokens is gone under a strong one)
+    tol = R.state_tol(200) + 2.0 ** -24 * min(80.0, -step * 200)
+    assert R.rel(pool, ref_p) <= tol
+    assert R.rel(out, ref_o) <= io_tol(x, entry) + tol
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e3, 1e8, 1e15, 1e25])
+def test_keys_that_grow_out_of_the_chunk(entry, io, size):
+    """Keys far from units, with which a chunk's inverse leaves fp32: the tokens in front know nothing of it."""
+    import torch
+    x = R.make([70, 3], Dk=64, Dv=64, io=io, seed=95)
+    ref_o, _ = R.delta(x, torch.zeros(x["v"].shape))
+    x["k"][30:64] = (x["k"][30:64].double() * size).to(x["k"].dtype)
+    out, _ = run(x, entry)
+    tol = io_tol(x, entry) + R.state_tol(70)
+    assert R.rel(out[:30], ref_o[:30]) <= tol and R.rel(out[70:], ref_o[70:]) <= tol
