@@ -106,10 +106,10 @@ constexpr int kNone = -1000;
 __device__ __forceinline__ int log2_floor(float x) {
   return x > 0.f && x < kInf ? static_cast<int>(__float_as_uint(x) >> 23) - 127 : kNone;
 }
-// the same within [-100, 100], 0 where there is none: for factors whose inverse is needed too
+// the same, at least -100, 0 where there is none: for factors whose inverse is needed too
 __device__ __forceinline__ int log2_near(float x) {
   const int e = log2_floor(x);
-  return e == kNone ? 0 : min(100, max(-100, e));
+  return e == kNone ? 0 : max(-100, e);
 }
 
 // Where fp16 operands are put.  fp16's smallest step is 2^-24, so a pair has its 22 bits for values
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PackedArgs a) {
       }
       *reinterpret_cast<hE *>(dst) = y;
       if constexpr (NP == 2) *reinterpret_cast<hE *>(dst + PART) = z;
-      if (which == 0 && !(m < 0x1p100f)) rest = kNaN;   // (a mark, as the values' factor: see by_token)
+      if (which == 0 && !(m < kInf)) rest = kNaN;   // (a mark, as the values' factor: see by_token)
       if ((tid & 15) == 0) {
         // (past the end rows of zeros stand in, whose norm without eps is 1 / 0: they weigh nothing)
         (which == 0 ? sk : su)[i] = i < n ? rest : 0.f;

@@ -359,6 +359,7 @@ int gdr_chunk_fwd_impl(const gdr_desc_t *desc);
  *  - NaN and infinities stay within their sequence and value heads and reach no earlier token; those
  *    of v and of a state's row stay in that value channel (but for the output norm, which joins a
  *    row's channels), those of q in that token's rows.
+ *  - qk_norm sums squares in fp32: q and k are below 1e19 there.
  *  - log_alpha <= 0; -inf (a reset) is exact: decays below exp(-200) per token are zero in fp32.
  * ------------------------------------------------------------------------------------------ */
 enum { GDR_F16 = 2 };   /* io_dtype: the packed and norm entry points also take fp16 */
@@ -461,11 +462,12 @@ typedef struct gdr_norm_desc {
  *   weight             [D] io_dtype, or NULL (ones)
  *   y                  [rows, D] io_dtype; or, in 8 bits, codes whose value is code * scales[row]
  *   scales             [rows] fp32, iff out_kind is 8 bits: max |y| / 127 (int8) or / 448 (e4m3);
- *                      0 for a row of zeros (its codes are 0), NaN where a y is NaN, else infinite where
- *                      one is infinite (the finite ones' codes are 0)
+ *                      0 where that is below 2^-126, as for a row of zeros (its codes are 0); NaN
+ *                      where a y is NaN, else infinite where one is (the finite ones' codes are 0)
  *   residual_out       [rows, D] io_dtype, x + residual rounded; required iff residual is given.
  *                      May be the same pointer as x or residual, with the same row stride.
- * The norm is taken of the fp32 sum.  y may be x where the types and strides agree and there is
+ * The norm is taken of the fp32 sum, whose squares are summed in fp32 too (a row of sqrt(D) |h| above
+ * 1.8e19 comes out as zeros).  y may be x where the types and strides agree and there is
  * no residual.  Any other overlap of an output with an input or another output is rejected.
  */
 gdr_status_t gdr_rms_norm(const gdr_norm_desc_t *desc, const void *x, const void *residual,

@@ -286,3 +286,16 @@ def test_keys_that_grow_out_of_the_chunk(entry, io, size):
     out, _ = run(x, entry)
     tol = io_tol(x, entry) + R.state_tol(70)
     assert R.rel(out[:30], ref_o[:30]) <= tol and R.rel(out[70:], ref_o[70:]) <= tol
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e10, 1e25, 1e31, 1e37])
+def test_huge_keys_under_the_norm(io, size):
+    """Chunked, each row on its own scale: up to the type's largest (sums of squares would end at 1e19)."""
+    import torch
+    x = R.make([70, 2], Dk=64, Dv=32, io=io, qk_norm=True, seed=87)
+    for n in "qk":
+        x[n] = (x[n].double() / x[n].double().abs().amax(-1, keepdim=True) * size).to(x[n].dtype)
+    out, pool = run(x, "mfma")
+    ref_o, ref_p = R.delta(normalised(x, 1e-6), torch.zeros(x["v"].shape))
+    assert R.rel(pool, ref_p) <= R.state_tol(70) and R.rel(out, ref_o) <= io_tol(x, "mfma") + R.state_tol(70)
