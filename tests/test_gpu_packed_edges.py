@@ -299,3 +299,26 @@ def test_huge_keys_under_the_norm(io, size):
     out, pool = run(x, "mfma")
     ref_o, ref_p = R.delta(normalised(x, 1e-6), torch.zeros(x["v"].shape))
     assert R.rel(pool, ref_p) <= R.state_tol(70) and R.rel(out, ref_o) <= io_tol(x, "mfma") + R.state_tol(70)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("heads,dims,shift", [((2, 6), (72, 24), 3), ((20, 40), (128, 64), 1), ((40, 40), (64, 48), 0), ((1, 2), (8, 8), 1)],
+                         ids=str)
+def test_some_columns_token_by_token(entry, io, heads, dims, shift):
+    """States of 1e8 in some value channels, reset in the first and in the third chunk, over views of a wider
+    projection, pooled slots and more workgroups than CUs: each channel to its own size, and the rows."""
+    import torch
+    from test_gpu_packed import call
+    x = R.make([200, 70, 1, 0, 66], Hk=heads[0], Hv=heads[1], Dk=dims[0], Dv=dims[1], io=io, slots=7, index=[6, 0, 3, 2, 1],
+               qk_norm=True, seed=96)
+    x["pool"][:, :, 3::16] *= 1e8
+    for start in (0, 128, 200, 271):
+        x["log_alpha"][start + 30] = float("-inf")
+    out, pool = (t.cpu() for t in call(x, entry, wide=True, shift=shift))
+    ref_o, ref_p = R.delta(x, torch.full(x["v"].shape, 7.0))
+    for c in range(dims[1]):
+        assert R.rel(pool[[6, 0, 1], :, c], ref_p[[6, 0, 1], :, c]) <= 2 * R.state_tol(200), c
+    assert torch.equal(pool[[2, 4, 5]], x["pool"][[2, 4, 5]])
+    after = [i for i in range(337) if 30 <= i < 200 or 230 <= i < 270 or i >= 301]
+    assert R.rel(out[after], ref_o[after]) <= io_tol(x, entry) + 2 * R.state_tol(200)
