@@ -284,7 +284,8 @@ def gdr_packed_fwd(q, k, v, cu_seqlens, *, beta, log_alpha=None, state=None, sta
     sequence s has slot s; negative: the sequence is skipped); ``has_state`` [n] bool, False
     starts from zeros.  ``qk_norm`` divides q and k by their L2 norms.  ``norm_weight`` [Dv] and
     ``norm_gate`` [N, Hv, Dv] apply the output norm.  ``impl``: "auto", "generic" (token by
-    token) or "mfma" (chunked).  ``workspace``: a uint8 tensor of
+    token) or "mfma" (chunked).  Rows of ``out`` in no sequence, and of skipped ones, are not
+    written (undefined in an ``out`` made here).  ``workspace``: a uint8 tensor of
     ``gdr_packed_fwd_workspace_size`` bytes, allocated when not given.  ``stream``: the stream to
     launch on (the current one by default).
     """

@@ -19,26 +19,27 @@
 // waves, from q^ and P fragments that they load from the workspace.
 //
 // What bounds it (bf16, Dk = Dv = 128).  The pass through the chunks is a chain: one sequence of 32768
-// tokens with 32 heads takes 860 us, 3950 cycles a chunk, of which the main wave's 82 products
+// tokens with 32 heads takes 870 to 930 us, some 4100 cycles a chunk, of which the main wave's 82 products
 // are some 1300, its fp16 splits and the operands' way from LDS the rest; with 4 sequences of
-// 4096 tokens and 16 heads (140 us, one workgroup a CU) the chain is the same and the CUs are all taken.
-// The preparation moves 0.88 GB for those 32768 tokens in 237 us (3.7 TB/s): bound by its own
+// 4096 tokens and 16 heads (144 us, one workgroup a CU) the chain is the same and the CUs are all taken.
+// The preparation moves 0.88 GB for those 32768 tokens in 250 us (3.5 TB/s): bound by its own
 // arithmetic (four workgroups a CU hide its loads) and its records' way out.  Short sequences pay
 // two launches and the first chunk's loads: 23 of 65 tokens on average with 8 heads 13 + 30 us.
 // Tried and slower: queries through LDS with the keys (1610 us for the long sequence, their small
 // scattered loads held everything up); the helpers' values in the main waves (1230 us, 1360 before);
 // shuffles through LDS for the column maxima (150 cycles each).
 //
-// Precision.  States are as exact as fp32 makes them: k^ and q^ are exact in fp16 (but for entries
+// Precision.  States are as exact as fp32 makes them, in every io type: k^ and q^ are exact in fp16 (but for entries
 // below 2^-21 of a key's largest), everything else on the state's path is a pair of fp16 values, 22
 // bits.  The pairs need their values within fp16's range, so the wave keeps its columns under a
 // power-of-two scale F per column (the recurrence is linear in each value column), set anew for
 // every chunk: a pair is off by 2^-22 of the column's largest value.
 // Where sizes in a column differ so much that this would show (a reset of a large state, one value far above
 // the others), the chunk goes token by token in fp32 (by_token, in the main wave, 0.8 us a token); kFar below
-// says when.  Asking costs 1 % under decays of e^-5 a chunk, 5 % under e^-10, 15 % under e^-100 (4 x 4096
-// tokens, a call: 215, 220 and 245 us; 213 unasked).
-// So does a chunk with an infinity or a NaN in its keys, values, gains or decays: what is not finite then reaches no earlier token and no other column.
+// says when.  Asking costs a call 1 % under decays of e^-5 a chunk, 5 % under e^-10, 15 to 20 % under e^-150 (32768
+// tokens: 1179, 1224 and 1340 us; unasked 1156, 1163 and 1149), fp32 up to 35 %.
+// So does a chunk with an infinity or a NaN in its keys, values, gains or decays: what is not finite then
+// reaches no earlier token and no other column.
 // Sums are fp32, the cumulative decay is summed in 64 bits and kept as two fp32 values (its differences
 // matter beside its size).
 #include <type_traits>

@@ -9,10 +9,10 @@
 // so a token needs one look at the state.  A workgroup holds 128 rows of one (sequence, head) in
 // registers (16 lanes a row, 8 rows a lane at most) for all of the sequence's tokens and touches
 // the pool once at each end: bound by HBM, 8 Dv Dk bytes a (sequence, head).
-// Measured: 64 sequences x 32 heads of 128 x 128, one token each, 43 us for 270 MB (6.3 TB/s, part of the
-// reads from the last-level cache); one sequence 7.1 us (latency: a load of the token, the
-// state and one row sum after another); 96 sequences x 12 heads of 64 x 64 with 1 to 5 tokens 16 us, bound by
-// its instructions a token.  8 rows a lane: the state of a workgroup is 64 KB of registers, three
+// Measured: 64 sequences x 32 heads of 128 x 128, one token each, 270 MB: 43 us in a loop over one pool
+// (6.3 TB/s, half of the reads from the last-level cache), 61 over four pools in turn (4.4 TB/s); one
+// sequence 7.1 us (latency: a load of the token, the state and one row sum after another); 96 sequences
+// x 12 heads of 64 x 96 with 1 to 4 tokens 16 us, bound by its instructions a token.  8 rows a lane: the state of a workgroup is 64 KB of registers, three
 // workgroups a CU under way (five of half the size with 64 columns).
 // The output norm needs all Dv rows of a head: it is fused up to 256, with twice the threads from 129 on
 // (as a pass of its own it would read a rounded o: 1.4 times the error of one rounding).
@@ -236,7 +236,9 @@ hipError_t launch_io(const PackedArgs &a, hipStream_t s) {
 
 // The output norm as a pass of its own, in place: for the chunked kernel, whose workgroups hold 32 of a
 // row's columns, and for Dv > 256.  A row is (token, head), 64 lanes a row, Dv <= 512; it reads and
-// writes what the kernel before left in the caches.
+// writes what the kernel before left in the caches.  So o is rounded to the io type before its norm as well,
+// 1.4 times the error of one rounding: kept in fp32 it would need a workspace of another 4 Dv bytes a token
+// and head, which the workspace's size, a matter of the descriptor alone, would ask of every call.
 template <typename IO>
 __device__ __forceinline__ void norm_row(const PackedArgs &a, int t, int h, int lane) {
   int s = t;

@@ -14,7 +14,8 @@
 // (5.4 TB/s); 8 rows of 4096 4.8 us, where the call from Python takes 8.7.  Over 64 to 16384 channels
 // 33 M elements run at 6.0 to 6.6 TB/s where the lanes are filled and rows start on 16 bytes, 4.7 to 6 elsewhere
 // (the last-level cache holds a part).  Gradient: 8191 x 2048 24 us, and 65537 x 128 gated (fp16) 18 us,
-// 5 and 4 more for the weight's sum.
+// 5 and 4 more for the weight's sum; 2.7 to 3.5 TB/s at widths that leave lanes idle or whose rows end inside a
+// load (300, 700, 1300, 2304, 5000, 7001, 12000 channels), against 5 to 5.5 at 1024, 2048 and 4096.
 #include <type_traits>
 
 #include "packed.h"
@@ -184,7 +185,8 @@ __global__ __launch_bounds__(threads_of(LANES)) void norm_kernel(NormArgs a) {
     const int c = (i * LANES + l) * V;
     uint32_t w[V / 4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {   // y / s to the last bit or so: a product, and its rest
+    for (int e = 0; e < V; ++e) {   // y / s to the last bit or so: a product, and its rest (16-bit inputs make
+                                     // exact ties often, one code in 10^5: these go by y's own fp32 roundings)
       const float c0 = h[i][e] * inv;
       h[i][e] = fmaf(fmaf(-c0, step, h[i][e]), inv, c0);
     }
